@@ -100,6 +100,8 @@ extern "C" {
 #define TQ_STATUS_NORM_SATURATED 1u
 #define TQ_STATUS_NONFINITE 2u
 #define TQ_STATUS_TIMEOUT 4u   /* a bounded wait inside a kernel gave up */
+#define TQ_STATUS_NO_PAGES 8u  /* tq_page_tables could not place a request */
+#define TQ_STATUS_BAD_PAGE 16u /* a page or slot outside the page storage */
 
 typedef enum tq_status {
     TQ_OK = 0,
@@ -117,7 +119,8 @@ typedef enum tq_rot_kind {
 
 typedef enum tq_dtype {
     TQ_DTYPE_F32 = 0,
-    TQ_DTYPE_BF16 = 1
+    TQ_DTYPE_BF16 = 1,
+    TQ_DTYPE_F16 = 2  /* tq_prompt_attention and tq_tree_attention only */
 } tq_dtype;
 
 typedef struct tq_rotation tq_rotation; /* opaque; owns its device copy */
@@ -455,6 +458,171 @@ tq_status tq_search_topk(const tq_rotation * rot, int32_t bits, int32_t block,
                          const uint16_t * db_norms, int64_t n_db, int32_t k, float * top_scores,
                          int32_t * top_rows, void * workspace, size_t workspace_bytes,
                          void * stream);
+
+/*
+ * Serving a paged cache: the four calls below are the steps of a serving loop
+ * around tq_decode_append_paged.  tq_page_tables turns request lengths into
+ * block tables and slot maps; tq_quantize_kv_paged writes new K / V rows
+ * through a slot map; tq_prompt_attention computes the attention of whole
+ * prompts from their unquantized rows; tq_tree_attention attends drafted
+ * tokens (or any new tokens) of every request over its cache.  All lengths are
+ * device arrays, so a step can be captured in a CUDA graph once and replayed
+ * with other lengths.  The pages have no counterpart of the four ([G] sec. 5.2
+ * names the KV-cache allocation only); layouts are those of
+ * tq_decode_append_paged.
+ */
+
+/*
+ * tq_page_tables -- block tables and slot maps from request lengths, on
+ * `stream`.  Request b holds ctx_lens[b] tokens (ceil(ctx / page_size) pages,
+ * already in its block-table row) and gets new_lens[b] more.  With
+ * held = ceil(ctx / P), want = ceil((ctx + new) / P) and need = want - held,
+ * the requests take pages from the front of the free list in request order,
+ * and token i of request b lies at position ctx + i, in
+ *   slot = block_table[b][(ctx + i) / P] * P + (ctx + i) % P.
+ *   ctx_lens, new_lens: device int32 [batch]; a negative length counts as 0.
+ *               1 <= batch <= 16384.
+ *   page_size:  a power of two in [16, 65536]; n_pages: pages of the storage.
+ *   free_pages: device int32 [n_free] (NULL only with n_free == 0).
+ *   block_table: device int32 [batch][max_pages]; entries held .. want - 1 of a
+ *               placed request are written, all others are left as they are.
+ *   cu_new:     device int32 [batch + 1], out: token offsets, cu_new[b] = sum of
+ *               the new lengths before b (saturating at 2^31 - 1).
+ *   total_lens: device int32 [batch], out: ctx + new of a placed request, ctx of
+ *               one that was not placed.
+ *   slots:      device int64 [n_slots], out: slots of request b's tokens at
+ *               cu_new[b] ..; -1 from cu_new[batch] on and for tokens of a
+ *               request that was not placed.
+ *   positions:  device int32 [n_slots] or NULL, out: token positions, -1 where
+ *               the slot is -1 for these two reasons.
+ *   n_taken:    device int32 [1], out: pages taken; free_pages[0 .. n_taken) now
+ *               belong to the requests.
+ *   status_dev: device uint32 or NULL.
+ * A request is placed if its pages fit its table row (want <= max_pages), its
+ * tokens fit the slot map (cu_new[b + 1] <= n_slots), ctx + new < 2^31, and the
+ * pages needed up to and including it fit the free list; otherwise none of its
+ * pages are taken and TQ_STATUS_NO_PAGES is set (requests after one that found
+ * the list too short are placed only if they need no page).  A token whose page
+ * (an entry of the table or of the free list) lies outside [0, n_pages) gets slot
+ * -1 and sets TQ_STATUS_BAD_PAGE.
+ */
+tq_status tq_page_tables(const int32_t * ctx_lens, const int32_t * new_lens, int32_t batch,
+                         int32_t page_size, int32_t n_pages, const int32_t * free_pages,
+                         int32_t n_free, int32_t * block_table, int32_t max_pages,
+                         int32_t * cu_new, int32_t * total_lens, int64_t * slots,
+                         int32_t * positions, int32_t n_slots, int32_t * n_taken,
+                         uint32_t * status_dev, void * stream);
+
+/*
+ * tq_quantize_kv_paged -- tq_quantize_kv with the rows stored through a slot map,
+ * on `stream`: row (token i, head h) of x [n_tokens][n_kv_heads][head_dim] goes to
+ * page slots[i] / page_size, token slots[i] % page_size of head h.
+ *   slots:      device int64 [n_tokens] (from tq_page_tables); a token with a
+ *               negative slot is not stored (padding, a rejected draft), nor is
+ *               one whose slot lies past the storage (TQ_STATUS_BAD_PAGE).  Slots
+ *               of stored tokens must differ from one another.
+ *   x:          device, contiguous, 16-byte aligned, F32 or BF16.
+ *   codes, norms: page storage as in tq_decode_append_paged, 16-byte aligned.
+ * Block 32, fp16 norms, default code order; codes and norms are bit for bit those
+ * of tq_quantize_kv.  n_tokens * n_kv_heads < 2^31; n_tokens == 0 is a no-op.
+ */
+tq_status tq_quantize_kv_paged(const tq_rotation * rot, int32_t bits, int32_t block,
+                               const float * centroids, const float * boundaries, const void * x,
+                               tq_dtype dtype, int64_t n_tokens, int32_t n_kv_heads,
+                               int32_t head_dim, const int64_t * slots, int32_t page_size,
+                               int32_t n_pages, uint32_t * codes, uint16_t * norms,
+                               uint32_t * status_dev, void * stream);
+
+/*
+ * tq_prompt_attention -- causal attention of packed sequences over their own
+ * unquantized keys and values, on `stream` ([T] sec. 4.3: softmax(Q K^T /
+ * sqrt(d)) V).  Sequence b has nq = cu_q[b + 1] - cu_q[b] queries and
+ * nk = cu_k[b + 1] - cu_k[b] keys; its query i attends its keys
+ * j <= i + nk - nq (the last query sees every key: with nq < nk the queries are
+ * the last chunk of a longer prompt).  A query that may attend no key
+ * (i + nk - nq < 0) gets zeros.  Keys that a query may not attend do not touch
+ * its output, whatever they hold (NaN and infinities included).
+ *   q:          device [total_q][n_q_heads][head_dim] of dtype, rows of one token
+ *               contiguous, tokens q_stride elements apart.
+ *   k, v:       device [total_k][n_kv_heads][head_dim], tokens k_stride and
+ *               v_stride elements apart (views of one fused projection work).
+ *               16-byte aligned; strides multiples of 8 and at least the row.
+ *   dtype:      TQ_DTYPE_BF16 or TQ_DTYPE_F16, of q, k, v and out.
+ *   cu_q, cu_k: device int32 [batch + 1], non-decreasing, from 0 to at most
+ *               total_q / total_k (values outside are clamped into the arrays);
+ *               cu_k NULL = cu_q.
+ *   scale:      <= 0 selects 1/sqrt(head_dim).
+ *   out:        device [total_q][n_q_heads][head_dim] of dtype, contiguous, 16-byte
+ *               aligned; rows from cu_q[batch] on are left as they are.
+ *   status_dev: device uint32 or NULL (TQ_STATUS_TIMEOUT).
+ * head_dim 64 / 128 / 256; n_q_heads a multiple of n_kv_heads; any group size.
+ * Scores and sums are fp32; the probabilities enter the second product rounded
+ * to dtype, the sum that divides them does not.
+ */
+tq_status tq_prompt_attention(const void * q, const void * k, const void * v, tq_dtype dtype,
+                              const int32_t * cu_q, const int32_t * cu_k, int32_t batch,
+                              int64_t total_q, int64_t total_k, int32_t n_q_heads,
+                              int32_t n_kv_heads, int32_t head_dim, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, float scale, void * out,
+                              uint32_t * status_dev, void * stream);
+
+/*
+ * tq_tree_workspace_size -- device workspace bytes of tq_tree_attention for up
+ * to these sizes on the CURRENT device (the split of the caches depends on its
+ * SM count); 0 for sizes the call refuses.
+ */
+size_t tq_tree_workspace_size(int32_t batch, int32_t n_rows, int32_t max_nodes,
+                              int32_t n_q_heads, int32_t n_kv_heads, int64_t max_len,
+                              int32_t head_dim);
+
+/*
+ * tq_tree_attention -- attention of the newest tokens of every request over its
+ * paged, packed cache, on `stream`: drafted tokens that form a tree, a chain of
+ * new tokens, or single tokens of requests whose lengths differ.
+ * Request b has n = cu_nodes[b + 1] - cu_nodes[b] nodes and lens[b] cached tokens,
+ * its nodes among them (stored before this call, by tq_quantize_kv_paged for
+ * instance): node j is token lens[b] - n + j.  Node i attends every token before
+ * the nodes (t < lens[b] - n), and node j
+ *   where bit j % 64 of tree_mask[row][j / 64] is set (row = cu_nodes[b] + i), or,
+ *   with tree_mask NULL, where j <= i.
+ *   out[row][h] = R^T sum_t softmax_t(scale <R q[row][h], k_hat_t>) v_hat_t
+ * with k_hat and v_hat as tq_decode_attention reads them; a node that attends
+ * nothing gets zeros.
+ *   q:          device [n_rows][n_q_heads][head_dim] of q_dtype (F32, BF16 or F16),
+ *               contiguous, 16-byte aligned.  Rows from cu_nodes[batch] on are
+ *               padding: neither read nor written.
+ *   cu_nodes:   device int32 [batch + 1], non-decreasing, from 0 to at most n_rows,
+ *               at most max_nodes apart (1 <= max_nodes <= 256; nodes from
+ *               max_nodes on are left out; offsets are clamped to [0, n_rows]).
+ *   lens:       device int32 [batch], 0 .. max_len (clamped); max_len <=
+ *               max_pages * page_size.
+ *   tree_mask:  device uint64 [n_rows][mask_words] or NULL; mask_words >=
+ *               ceil(max_nodes / 64).
+ *   block_table, page_size, n_pages, k_*, v_*: as in tq_decode_append_paged
+ *               (entries outside [0, n_pages) are clamped).
+ *   out:        device [n_rows][n_q_heads][head_dim] of q_dtype, 16-byte aligned.
+ *   workspace:  >= tq_tree_workspace_size(...) bytes for these sizes, 256-byte
+ *               aligned, needs no initialisation; calls that may overlap need one
+ *               each.
+ *   status_dev: device uint32 or NULL (TQ_STATUS_TIMEOUT).
+ * Block 32 with fp16 norms, default code order, keys without QJL signs.  The
+ * rotated queries and the dequantized rows enter the products as fp16, sums are
+ * fp32.  A cached token whose K or V norm is NaN or infinite makes the nodes that
+ * attend it NaN, and no others.
+ */
+tq_status tq_tree_attention(const tq_rotation * rot, int32_t k_bits, int32_t v_bits,
+                            int32_t block, const float * k_centroids,
+                            const float * v_centroids, const void * q, tq_dtype q_dtype,
+                            const int32_t * cu_nodes, int32_t batch, int32_t n_rows,
+                            int32_t max_nodes, const int32_t * lens, int64_t max_len,
+                            const uint64_t * tree_mask, int32_t mask_words,
+                            int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                            int32_t page_size, int32_t n_pages, const int32_t * block_table,
+                            int32_t max_pages, const uint32_t * k_codes,
+                            const uint16_t * k_norms, const uint32_t * v_codes,
+                            const uint16_t * v_norms, float scale, void * out,
+                            void * workspace, size_t workspace_bytes, uint32_t * status_dev,
+                            void * stream);
 
 /* Static string for a status code. */
 const char * tq_status_string(tq_status s);

@@ -13,8 +13,11 @@ from ._lib import (  # noqa: F401
     FMT_NORM_CORRECTED,
     FMT_NORM_F32,
     FORMAT_VERSION,
+    STATUS_BAD_PAGE,
+    STATUS_NO_PAGES,
     STATUS_NONFINITE,
     STATUS_NORM_SATURATED,
+    STATUS_TIMEOUT,
     TQError,
     Rotation,
     attn_logits,
@@ -27,8 +30,13 @@ from ._lib import (  # noqa: F401
     decode_workspace_size,
     exported_symbols,
     lib_path,
+    page_tables,
+    prompt_attention,
     quantize_kv,
+    quantize_kv_paged,
     rotation_generate,
     search_topk,
     search_workspace_size,
+    tree_attention,
+    tree_workspace_size,
 )

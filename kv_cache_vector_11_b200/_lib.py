@@ -18,12 +18,15 @@ _lib = ctypes.CDLL(_LIB_PATH)
 FORMAT_VERSION = 1
 STATUS_NORM_SATURATED = 1
 STATUS_NONFINITE = 2
+STATUS_TIMEOUT = 4
+STATUS_NO_PAGES = 8
+STATUS_BAD_PAGE = 16
 FMT_NORM_F32 = 1
 FMT_NORM_CORRECTED = 2
 FMT_GROUPED = 4
 
 ROT_KINDS = {"wht": 0, "haar": 1, "gauss": 2}
-DTYPES = {"f32": 0, "bf16": 1}
+DTYPES = {"f32": 0, "bf16": 1, "f16": 2}
 
 _c = ctypes
 _vp = _c.c_void_p
@@ -64,6 +67,16 @@ _SIGS = {
     "tq_search_workspace_size": (_c.c_size_t, [_i32, _i64, _i32, _i32]),
     "tq_search_topk": (_i32, [_vp, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _i64, _i32,
                               _vp, _vp, _vp, _c.c_size_t, _vp]),
+    "tq_page_tables": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp,
+                              _i32, _vp, _vp, _vp]),
+    "tq_quantize_kv_paged": (_i32, [_vp, _i32, _i32, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp,
+                                    _i32, _i32, _vp, _vp, _vp, _vp]),
+    "tq_prompt_attention": (_i32, [_vp, _vp, _vp, _i32, _vp, _vp, _i32, _i64, _i64, _i32, _i32, _i32,
+                                   _i64, _i64, _i64, _c.c_float, _vp, _vp, _vp]),
+    "tq_tree_workspace_size": (_c.c_size_t, [_i32, _i32, _i32, _i32, _i32, _i64, _i32]),
+    "tq_tree_attention": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32,
+                                 _vp, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i32,
+                                 _vp, _vp, _vp, _vp, _c.c_float, _vp, _vp, _c.c_size_t, _vp, _vp]),
     "tq_status_string": (_c.c_char_p, [_i32]),
     "tq_last_error": (_c.c_char_p, []),
 }
@@ -362,4 +375,186 @@ def decode_append_paged(rot, k_bits, v_bits, k_codebook, v_codebook, q, k_new, v
             _ptr(pages["v_codes"]), _ptr(pages["v_norms"]), float(scale), _ptr(out),
             _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
             _stream_ptr(stream, q.device)), "tq_decode_append_paged")
+    return out
+
+
+def _require(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _dtype_code16(t):
+    """As _dtype_code, and fp16 (prompt and tree attention)."""
+    import torch
+    return DTYPES["f16"] if t.dtype == torch.float16 else _dtype_code(t)
+
+
+def _int_array(t, n, name, device, kind="int32"):
+    """A contiguous integer array of n entries on ``device`` (the kernels read
+    it without further checks)."""
+    import torch
+    _require(t.dtype == getattr(torch, kind) and t.is_contiguous() and t.numel() == n and
+             t.device == device, f"{name}: contiguous {kind} of {n} entries on {device}")
+
+
+def page_tables(ctx_lens, new_lens, page_size, n_pages, free_pages, block_table, n_slots, out=None,
+                status=None, stream=None):
+    """Block tables and slot maps from request lengths: request b holds
+    ctx_lens[b] tokens and gets new_lens[b] more (int32 [batch], CUDA).  Pages
+    come from the front of ``free_pages`` (int32 [n_free]) in request order and
+    are written into ``block_table`` (int32 [batch, max_pages]) in place.
+
+    Returns dict(cu_new int32 [batch + 1], total_lens int32 [batch], slots
+    int64 [n_slots], positions int32 [n_slots], n_taken int32 [1]); slots and
+    positions are -1 past the last token and for requests that were not placed
+    (STATUS_NO_PAGES in ``status``).  ``out`` may supply those tensors."""
+    import torch
+    dev = ctx_lens.device
+    batch = ctx_lens.shape[0]
+    if out is None:
+        out = {"cu_new": torch.empty((batch + 1,), dtype=torch.int32, device=dev),
+               "total_lens": torch.empty((batch,), dtype=torch.int32, device=dev),
+               "slots": torch.empty((n_slots,), dtype=torch.int64, device=dev),
+               "positions": torch.empty((n_slots,), dtype=torch.int32, device=dev),
+               "n_taken": torch.empty((1,), dtype=torch.int32, device=dev)}
+    _int_array(ctx_lens, batch, "ctx_lens", dev)
+    _int_array(new_lens, batch, "new_lens", dev)
+    _int_array(free_pages, free_pages.numel(), "free_pages", dev)
+    _int_array(out["cu_new"], batch + 1, "cu_new", dev)
+    _int_array(out["total_lens"], batch, "total_lens", dev)
+    _int_array(out["slots"], n_slots, "slots", dev, "int64")
+    _int_array(out["n_taken"], 1, "n_taken", dev)
+    positions = out.get("positions")
+    if positions is not None:
+        _int_array(positions, n_slots, "positions", dev)
+    _require(block_table.dim() == 2 and block_table.shape[0] == batch, "block_table: [batch, max_pages]")
+    _int_array(block_table, block_table.numel(), "block_table", dev)
+    with _on(dev):
+        _check(_lib.tq_page_tables(
+            _ptr(ctx_lens), _ptr(new_lens), batch, page_size, n_pages, _ptr(free_pages),
+            free_pages.numel(), _ptr(block_table), block_table.shape[1], _ptr(out["cu_new"]),
+            _ptr(out["total_lens"]), _ptr(out["slots"]), _ptr(positions), n_slots,
+            _ptr(out["n_taken"]), _ptr(status), _stream_ptr(stream, dev)), "tq_page_tables")
+    return out
+
+
+def quantize_kv_paged(rot, bits, centroids, boundaries, x, slots, codes, norms, page_size, block=32,
+                      status=None, stream=None):
+    """Quantize rows x [n_tokens, n_kv_heads, head_dim] (bf16 or fp32, CUDA)
+    into page storage: token i goes to ``slots[i]`` (int64, as page_tables
+    returns them; negative = not stored) of ``codes`` int32 [n_pages,
+    n_kv_heads, page_size, W] and ``norms`` int16 [n_pages, n_kv_heads,
+    page_size, head_dim / 32].  Same bits as ``quantize_kv``."""
+    import torch
+    n, heads, d = x.shape
+    dev = x.device
+    n_pages = codes.shape[0]
+    w = max(code_words_per_row(bits, block, d), 0)
+    _require(x.is_contiguous(), "x: contiguous [n_tokens, n_kv_heads, head_dim]")
+    _int_array(slots, n, "slots", dev, "int64")
+    _require(tuple(codes.shape) == (n_pages, heads, page_size, w) and codes.dtype == torch.int32 and
+             codes.is_contiguous() and codes.device == dev, f"codes: int32 [n_pages, {heads}, {page_size}, {w}]")
+    _require(tuple(norms.shape) == (n_pages, heads, page_size, d // 32) and norms.dtype == torch.int16 and
+             norms.is_contiguous() and norms.device == dev,
+             f"norms: int16 [{n_pages}, {heads}, {page_size}, {d // 32}]")
+    c = np.ascontiguousarray(centroids, dtype=np.float32)
+    t = np.ascontiguousarray(boundaries, dtype=np.float32)
+    with _on(dev):
+        _check(_lib.tq_quantize_kv_paged(
+            rot.handle, bits, block, c.ctypes.data, t.ctypes.data, _ptr(x), _dtype_code(x), n, heads,
+            d, _ptr(slots), page_size, n_pages, _ptr(codes), _ptr(norms), _ptr(status),
+            _stream_ptr(stream, dev)), "tq_quantize_kv_paged")
+
+
+def prompt_attention(q, k, v, cu_q, cu_k=None, scale=0.0, out=None, status=None, stream=None):
+    """Causal attention of packed sequences: q [total_q, n_q_heads, head_dim],
+    k and v [total_k, n_kv_heads, head_dim] (bf16 or fp16, CUDA; the tokens may
+    be strided, as slices of a fused projection are), offsets cu_q and cu_k
+    int32 [batch + 1] (cu_k defaults to cu_q).  With fewer queries than keys
+    the queries are the last ones.  Returns out, of q's type and shape; rows
+    past cu_q[batch] are left as they are."""
+    import torch
+    total_q, n_q, d = q.shape
+    total_k, n_kv, _ = k.shape
+    dev = q.device
+    if out is None:
+        out = torch.empty((total_q, n_q, d), dtype=q.dtype, device=dev)
+    for name, t, n, h in (("q", q, total_q, n_q), ("k", k, total_k, n_kv), ("v", v, total_k, n_kv)):
+        _require(tuple(t.shape) == (n, h, d) and t.dtype == q.dtype and t.device == dev and
+                 t.stride(2) == 1 and (h == 1 or t.stride(1) == d),
+                 f"{name}: [{n}, {h}, {d}] rows of q's type, contiguous within a token")
+    _require(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous() and out.device == dev,
+             "out: contiguous, of q's shape and type")
+    batch = cu_q.numel() - 1
+    _int_array(cu_q, batch + 1, "cu_q", dev)
+    if cu_k is not None:
+        _int_array(cu_k, batch + 1, "cu_k", dev)
+    else:
+        _require(total_k == total_q, "cu_k is needed where k has another length than q")
+    strides = [t.stride(0) if t.shape[0] > 1 else t.shape[1] * d for t in (q, k, v)]
+    with _on(dev):
+        _check(_lib.tq_prompt_attention(
+            _ptr(q), _ptr(k), _ptr(v), _dtype_code16(q), _ptr(cu_q), _ptr(cu_k), batch, total_q,
+            total_k, n_q, n_kv, d, *strides, float(scale), _ptr(out), _ptr(status),
+            _stream_ptr(stream, dev)), "tq_prompt_attention")
+    return out
+
+
+def tree_workspace_size(batch, n_rows, max_nodes, n_q_heads, n_kv_heads, max_len, head_dim):
+    return int(_lib.tq_tree_workspace_size(batch, n_rows, max_nodes, n_q_heads, n_kv_heads, max_len,
+                                           head_dim))
+
+
+def tree_attention(rot, k_bits, v_bits, k_centroids, v_centroids, q, cu_nodes, lens, pages,
+                   block_table, page_size, max_nodes, max_len, tree_mask=None, scale=0.0, block=32,
+                   out=None, workspace=None, status=None, stream=None):
+    """Attention of each request's newest tokens over its paged cache: q
+    [n_rows, n_q_heads, head_dim] (bf16, fp16 or fp32, CUDA) holds request b's
+    nodes at rows cu_nodes[b] .. (int32 [batch + 1]), the cached tokens
+    lens[b] - n .. lens[b] - 1 of its ``lens[b]`` (int32 [batch], at most
+    ``max_len``).  Node i attends all tokens before the nodes and the nodes
+    whose bits are set in ``tree_mask`` (int64 [n_rows, words], 64 nodes to a
+    word); without a mask the nodes 0 .. i.  ``pages`` and ``block_table`` as
+    in decode_append_paged.  Returns out, of q's type and shape."""
+    import torch
+    n_rows, n_q, d = q.shape
+    dev = q.device
+    batch = lens.shape[0]
+    if out is None:
+        out = torch.empty((n_rows, n_q, d), dtype=q.dtype, device=dev)
+    _require(q.is_contiguous() and out.shape == q.shape and out.dtype == q.dtype and
+             out.is_contiguous() and out.device == dev, "q and out: contiguous, same shape and type")
+    _int_array(cu_nodes, batch + 1, "cu_nodes", dev)
+    _int_array(lens, batch, "lens", dev)
+    _require(block_table.dim() == 2 and block_table.shape[0] == batch, "block_table: [batch, max_pages]")
+    _int_array(block_table, block_table.numel(), "block_table", dev)
+    n_pages, n_kv = pages["k_codes"].shape[:2]
+    for name, bits in (("k", k_bits), ("v", v_bits)):
+        c, n = pages[name + "_codes"], pages[name + "_norms"]
+        w = max(code_words_per_row(bits, block, d), 0)
+        _require(tuple(c.shape) == (n_pages, n_kv, page_size, w) and c.dtype == torch.int32 and
+                 c.is_contiguous() and c.device == dev,
+                 f"{name}_codes: int32 [{n_pages}, {n_kv}, {page_size}, {w}]")
+        _require(tuple(n.shape) == (n_pages, n_kv, page_size, d // 32) and n.dtype == torch.int16 and
+                 n.is_contiguous() and n.device == dev,
+                 f"{name}_norms: int16 [{n_pages}, {n_kv}, {page_size}, {d // 32}]")
+    words = 0
+    if tree_mask is not None:
+        _require(tree_mask.dim() == 2, "tree_mask: [n_rows, words]")
+        words = tree_mask.shape[1]
+        _int_array(tree_mask, n_rows * words, "tree_mask", dev, "int64")
+    kc = np.ascontiguousarray(k_centroids, dtype=np.float32)
+    vc = np.ascontiguousarray(v_centroids, dtype=np.float32)
+    with _on(dev):
+        if workspace is None:
+            need = tree_workspace_size(batch, n_rows, max_nodes, n_q, n_kv, max_len, d)
+            workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
+        _check(_lib.tq_tree_attention(
+            rot.handle, k_bits, v_bits, block, kc.ctypes.data, vc.ctypes.data, _ptr(q),
+            _dtype_code16(q), _ptr(cu_nodes), batch, n_rows, max_nodes, _ptr(lens), max_len,
+            _ptr(tree_mask), words, n_q, n_kv, d, page_size, n_pages, _ptr(block_table),
+            block_table.shape[1], _ptr(pages["k_codes"]), _ptr(pages["k_norms"]),
+            _ptr(pages["v_codes"]), _ptr(pages["v_norms"]), float(scale), _ptr(out),
+            _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
+            _stream_ptr(stream, dev)), "tq_tree_attention")
     return out

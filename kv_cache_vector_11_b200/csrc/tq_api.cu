@@ -43,6 +43,11 @@ int ensure_dynamic_smem(const void * func, int bytes) {
     return 0;
 }
 
+bool aligned(const void * p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+bool supported_dim(int32_t d) { return d == 64 || d == 128 || d == 256; }
+bool supported_bits(int32_t b) { return b >= 2 && b <= 4; }
+
 namespace {
 
 uint16_t f32_to_bf16_bits(float f) {
@@ -61,10 +66,7 @@ float bf16_bits_to_f32(uint16_t h) {
     return f;
 }
 
-bool aligned(const void * p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-bool supported_dim(int32_t d) { return d == 64 || d == 128 || d == 256; }
-bool supported_bits(int32_t b) { return b >= 2 && b <= 4; }
+}  // namespace
 
 tq_status build_codebook_params(int32_t bits, const float * centroids, const float * boundaries,
                                 CodebookParams * out, bool need_boundaries) {
@@ -95,6 +97,8 @@ tq_status build_codebook_params(int32_t bits, const float * centroids, const flo
     return TQ_OK;
 }
 
+namespace {
+
 tq_status upload_dense(tq_rotation * r) {
     const size_t n = (size_t)r->rows * r->cols;
     std::vector<float> f(n);
@@ -123,6 +127,8 @@ tq_status upload_dense(tq_rotation * r) {
     return TQ_OK;
 }
 
+}  // namespace
+
 tq_status check_rotation(const tq_rotation * rot, int32_t head_dim) {
     if (!rot) return fail(TQ_ERR_INVALID_ARG, "rotation handle is NULL");
     if (rot->kind != TQ_ROT_WHT && rot->kind != TQ_ROT_HAAR)
@@ -133,6 +139,8 @@ tq_status check_rotation(const tq_rotation * rot, int32_t head_dim) {
     return TQ_OK;
 }
 
+namespace {
+
 tq_status check_qjl(const tq_rotation * qjl, int32_t head_dim) {
     if (!qjl) return TQ_OK;
     if (qjl->kind != TQ_ROT_GAUSS) return fail(TQ_ERR_INVALID_ARG, "qjl handle must be GAUSS");
@@ -142,12 +150,13 @@ tq_status check_qjl(const tq_rotation * qjl, int32_t head_dim) {
     return TQ_OK;
 }
 
+}  // namespace
+
 tq_status cuda_status(int err, const char * what) {
     if (err == 0) return TQ_OK;
     return fail(TQ_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString((cudaError_t)err));
 }
 
-}  // namespace
 }  // namespace tq
 
 namespace tq {
@@ -323,6 +332,55 @@ tq_status tq_quantize_kv_ex(const tq_rotation * rot, int32_t bits, int32_t block
     return cuda_status(launch_quantize(rot, qjl, bits, dtype == TQ_DTYPE_BF16, head_dim, cb, tab, a,
                                        stream),
                        "quantize launch");
+}
+
+tq_status tq_quantize_kv_paged(const tq_rotation * rot, int32_t bits, int32_t block,
+                               const float * centroids, const float * boundaries, const void * x,
+                               tq_dtype dtype, int64_t n_tokens, int32_t n_kv_heads,
+                               int32_t head_dim, const int64_t * slots, int32_t page_size,
+                               int32_t n_pages, uint32_t * codes, uint16_t * norms,
+                               uint32_t * status_dev, void * stream) {
+    tq_status st = check_rotation(rot, head_dim);
+    if (st != TQ_OK) return st;
+    if (!supported_bits(bits)) return fail(TQ_ERR_UNSUPPORTED, "bits must be 2, 3 or 4");
+    if (block != kBlock) return fail(TQ_ERR_UNSUPPORTED, "paged caches hold block 32 (fp16 norms)");
+    if (dtype != TQ_DTYPE_F32 && dtype != TQ_DTYPE_BF16)
+        return fail(TQ_ERR_INVALID_ARG, "unknown dtype");
+    if (n_tokens < 0 || n_kv_heads < 1) return fail(TQ_ERR_INVALID_ARG, "n_tokens < 0 or n_kv_heads < 1");
+    if (n_tokens > (int64_t)INT32_MAX / n_kv_heads)
+        return fail(TQ_ERR_UNSUPPORTED, "n_tokens * n_kv_heads above 2^31 - 1");
+    if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)) != 0)
+        return fail(TQ_ERR_UNSUPPORTED, "page_size must be a power of two in [16, 65536]");
+    if (n_pages < 1) return fail(TQ_ERR_INVALID_ARG, "n_pages must be >= 1");
+    CodebookParams cb;
+    if ((st = build_codebook_params(bits, centroids, boundaries, &cb, true)) != TQ_OK) return st;
+    if (n_tokens == 0) return TQ_OK;
+    if (!x || !slots || !codes || !norms) return fail(TQ_ERR_INVALID_ARG, "null x / slots / codes / norms");
+    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(norms, 16) || !aligned(slots, 8))
+        return fail(TQ_ERR_INVALID_ARG, "x, codes and norms must be 16-byte aligned, slots 8-byte");
+    QuantizeArgs a{};
+    a.x = x;
+    a.n_rows = n_tokens * n_kv_heads;
+    a.codes = codes;
+    a.norms = norms;
+    a.status = status_dev;
+    a.rot_f32 = rot->dev_f32;
+    a.rot_hi = rot->dev_hi;
+    a.rot_lo = rot->dev_lo;
+    a.inv_sqrt_d = 1.0f / std::sqrt((float)head_dim);
+    a.norm_block = block;
+    a.slots = slots;
+    a.slot_heads = n_kv_heads;
+    while ((1 << a.page_shift) < page_size) ++a.page_shift;
+    a.n_pages = n_pages;
+    for (int i = 0; i < (1 << bits); ++i) a.centroid_sq[i] = centroids[i] * centroids[i];
+    for (int i = 0; i < 16; ++i) a.boundary[i] = i < (1 << bits) - 1 ? boundaries[i] : 0.0f;
+    SearchTable tab;
+    std::string why;
+    if (!build_search_table(bits, boundaries, &tab, &why)) return fail(TQ_ERR_UNSUPPORTED, why);
+    return cuda_status(launch_quantize(rot, nullptr, bits, dtype == TQ_DTYPE_BF16, head_dim, cb, tab, a,
+                                       stream),
+                       "paged quantize launch");
 }
 
 static tq_status check_attn_common(const tq_rotation * rot, const tq_rotation * qjl,

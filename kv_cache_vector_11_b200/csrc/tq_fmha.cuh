@@ -1,0 +1,221 @@
+// Pieces of the tensor-core attention kernels (prompt and drafted-token
+// attention): tiles of 128 query rows against tiles of 128 keys, the scores and
+// the output accumulators in TMEM, one softmax thread per row.
+//
+// TMEM (512 columns, 128 lanes = the tile's rows): two score slots of 128 fp32
+// columns at 0 and 128, the output accumulators from column 256 on.  A row's
+// weights are written back as 16-bit pairs over the first 64 columns of its
+// score slot, which the second product reads as its A operand.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math_constants.h>
+
+#include <cstdint>
+
+#include "tq_tc.cuh"
+
+namespace tq {
+namespace fm {
+
+constexpr int kTile = 128;                     // rows of a query tile, keys of a key tile
+constexpr uint32_t kSlotCols = 128;            // TMEM columns of a score slot
+constexpr uint32_t kOutCol = 256;              // first column of the output accumulators
+constexpr uint64_t kWaitNs = 1000000000ull;    // bound of every wait
+
+// 32 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t * r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,"
+        "%27,%28,%29,%30,%31"
+        "}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr) : "memory");
+}
+
+// 128 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t * r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,"
+        "%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,"
+        "%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,"
+        "%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,%96,%97,%98,%99,%100,"
+        "%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,"
+        "%121,%122,%123,%124,%125,%126,%127"
+        "}, [%128];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
+          "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
+          "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
+          "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
+          "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
+          "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
+          "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
+          "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
+          "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+        : "r"(taddr) : "memory");
+}
+
+// 32 32-bit values into consecutive columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t * r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
+        "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
+        "%28,%29,%30,%31,%32"
+        "};"
+        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+           "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+           "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// D[tmem] (+)= A[tmem] B[smem], 16-bit A and B, fp32 D; A holds two values per
+// 32-bit column (16 of the contracted index in 8 columns).
+__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+        :: "r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+// Descriptor of a value tile as the second product's B operand: rows of 64
+// columns (128 bytes, 128-byte swizzle) per key, so the contracted index (the
+// key) is the strided one.  `slice` = bytes from one 64-column slice to the
+// next, 1024 bytes from one group of 8 keys to the next.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t slice) {
+    uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((slice >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// Instruction descriptor of kind::f16: fp32 D of 128 x n, A and B both fp16 or
+// both bf16, B with the contracted index strided when `mn` is set.
+__host__ __device__ constexpr uint32_t idesc(bool bf16, int n, bool mn) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(kTile >> 4) << 24);
+}
+
+// 2^x with the hardware approximation (relative error below 2^-22; -inf -> 0)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+// Running softmax of one row, in base 2: weights are 2^(s mul - ref + kShift).
+// `ref` is raised only when a row's maximum passes it by more than kLazy, so
+// that the accumulator is rescaled a few times a row instead of once a tile;
+// the factor 2^kLazy that a weight may exceed 1 by cancels in the quotient.
+// fp16 weights are kept 2^kShift larger (at most 2^15): what falls under the
+// type's normal range is then below 2^-21 of the row's largest weight.
+constexpr float kLazy = 8.0f;
+template <bool BF16>
+constexpr float kShift = BF16 ? 0.0f : 7.0f;
+
+struct RowState {
+    float ref;     // -inf until a key was seen
+    float sum;
+};
+
+// One tile of scores: reads slot `s_tm` (lane included), drops the columns
+// whose bit in `allowed` is clear (MASKED), updates the row's state, rescales
+// the accumulator at `o_tm` (o_cols columns) where needed -- after
+// wait_acc() says that the products of the tiles before are done -- and writes
+// the weights.  All 32 lanes of the warp call it together.
+template <bool BF16, bool MASKED, typename WaitAcc>
+__device__ __forceinline__ bool softmax_tile(uint32_t s_tm, uint32_t o_tm, int o_cols, bool first, float mul,
+                                             const uint32_t * allowed, RowState & st, WaitAcc wait_acc) {
+    uint32_t r[128];
+    tmem_ld128(s_tm, r);
+    if constexpr (MASKED) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+            if (!((allowed[c >> 5] >> (c & 31)) & 1u)) r[c] = 0xFF800000u;
+    }
+    float mx[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(r[i]);
+#pragma unroll
+    for (int c = 4; c < 128; c += 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            mx[i] = c + 4 + i < 128 ? fmaxf(fmaxf(mx[i], __uint_as_float(r[c + i])), __uint_as_float(r[c + 4 + i]))
+                                    : fmaxf(mx[i], __uint_as_float(r[c + i]));
+    }
+    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+    bool ok = true;
+    const bool raise = top > st.ref + kLazy;          // (ref = -inf: any finite score)
+    if (first) {
+        st.ref = top;
+    } else if (__any_sync(0xffffffffu, raise)) {
+        const float f = raise ? ex2(st.ref - top) : 1.0f;
+        if (raise) st.ref = top;
+        st.sum *= f;
+        ok = wait_acc();
+        tc::fence_after_sync();
+        for (int c = 0; c < o_cols; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_tm + (uint32_t)c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(o_tm + (uint32_t)c, o);
+        }
+    }
+    const float bias = kShift<BF16> - (st.ref == -CUDART_INF_F ? 0.0f : st.ref);
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+            const float a = ex2(fmaf(__uint_as_float(r[64 * h + c]), mul, bias));
+            const float b = ex2(fmaf(__uint_as_float(r[64 * h + c + 1]), mul, bias));
+            sum[c & 2] += a;
+            sum[(c & 2) + 1] += b;
+            w[c >> 1] = pack2<BF16>(a, b);
+        }
+        tmem_st32(s_tm + 32u * (uint32_t)h, w);
+    }
+    st.sum += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    tmem_wait_st();
+    tc::fence_before_sync();
+    return ok;
+}
+
+}  // namespace fm
+}  // namespace tq

@@ -54,6 +54,14 @@ int32_t device_sm_count();
 // the attribute is set at most once per size increase.  Returns a cudaError_t.
 int ensure_dynamic_smem(const void * func, int bytes);
 
+// Argument checks shared by the entry points (tq_api.cu).  cuda_status turns a
+// cudaError_t into a status with the error's name as the reason.
+bool aligned(const void * p, size_t a);
+bool supported_dim(int32_t d);
+bool supported_bits(int32_t b);
+tq_status check_rotation(const tq_rotation * rot, int32_t head_dim);
+tq_status cuda_status(int err, const char * what);
+
 // Kernel-side parameter blocks ------------------------------------------------
 
 constexpr int kBlock = 32;       // coordinates per norm block
@@ -63,6 +71,8 @@ struct CodebookParams {
     float centroid[kMaxLevels];        // ascending, 2^bits valid
     float pos_boundary[kMaxLevels / 2];  // boundaries > 0, ascending, 2^(bits-1) - 1 valid
 };
+tq_status build_codebook_params(int32_t bits, const float * centroids, const float * boundaries,
+                                CodebookParams * out, bool need_boundaries);
 
 // Uniform-grid search table for the quantizer.  Cells of width w (a power of
 // two below the smallest gap between boundaries) tile [-1 - w/2, 1 + w/2]; the
@@ -113,6 +123,10 @@ struct QuantizeArgs {
     float centroid_sq[16];
     float boundary[16];         // ascending decision boundaries (variants' binary search)
     int32_t grouped;            // codes in the lane-grouped row order (tensor-core kernel, d = 128)
+    // tq_quantize_kv_paged: slot of every token (NULL = rows stored in order),
+    // rows [token][slot_heads], pages of 2^page_shift tokens
+    const int64_t * slots;
+    int32_t slot_heads, page_shift, n_pages;
 };
 
 struct AttnArgs {
@@ -181,6 +195,11 @@ struct AppendParams {
 bool encode_tensor_map_2d(CUtensorMap * map, CUtensorMapDataType dtype, const void * base,
                           uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_inner,
                           uint32_t box_outer, CUtensorMapSwizzle swizzle);
+// The same for three dimensions: extents and box in elements, strides of the
+// second and third dimension in bytes.
+bool encode_tensor_map_3d(CUtensorMap * map, CUtensorMapDataType dtype, const void * base,
+                          const uint64_t * dims, const uint64_t * strides, const uint32_t * box,
+                          CUtensorMapSwizzle swizzle);
 
 // Warp-range decode plan (tq_attention.cu): whether the tensor-core path
 // applies, its grid and the partial slots per query head.

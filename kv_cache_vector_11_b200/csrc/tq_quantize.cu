@@ -242,6 +242,22 @@ __device__ __forceinline__ void store_words(uint32_t * dst, const uint32_t * w) 
     }
 }
 
+// Row of the page storage ([page][kv head][token]) that input row `row`
+// ([token][kv head]) goes to through the slot map, or -1 for a token that is not
+// stored (a negative slot; one past the storage also sets TQ_STATUS_BAD_PAGE).
+__device__ __forceinline__ int64_t paged_row(const QuantizeArgs & a, int64_t row, uint32_t & status) {
+    const uint32_t token = (uint32_t)row / (uint32_t)a.slot_heads;      // n_rows < 2^31 (checked)
+    const uint32_t head = (uint32_t)row - token * (uint32_t)a.slot_heads;
+    const int64_t slot = a.slots[token];
+    if (slot < 0) return -1;
+    const int64_t page = slot >> a.page_shift;
+    if (page >= a.n_pages) {
+        status |= TQ_STATUS_BAD_PAGE;
+        return -1;
+    }
+    return ((page * a.slot_heads + head) << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
+}
+
 // Norms, codes and stores for the lane's 64 rotated coordinates z of `row`.
 template <int D, int BITS>
 __device__ __forceinline__ void finish_row(const float2 * z, int64_t row, int q,
@@ -250,6 +266,10 @@ __device__ __forceinline__ void finish_row(const float2 * z, int64_t row, int q,
                                            float norm_scale, const QuantizeArgs & a,
                                            uint32_t & status, bool valid = true) {
     constexpr int NB = D / 32;
+    if (a.slots != nullptr && valid) {
+        row = paged_row(a, row, status);
+        valid = row >= 0;
+    }
     uint32_t words[2 * BITS];
     uint16_t nh[2];
 #pragma unroll
@@ -557,7 +577,8 @@ struct WtCfg {
     static_assert(RING % SPT == 0 && RING <= 8, "whole tiles in the ring, at most 8 slots");
 };
 
-template <int D, int BITS, bool DENSE, bool GROUPED = false>
+// PAGED: rows go to the page storage through the slot map (a.slots).
+template <int D, int BITS, bool DENSE, bool GROUPED = false, bool PAGED = false>
 __global__ void __launch_bounds__(WtCfg<D, BITS, DENSE>::THREADS, 1)
 quantize_rot_tc_kernel(const __grid_constant__ QuantizeArgs a,
                        const __grid_constant__ SearchTable st,
@@ -704,8 +725,14 @@ quantize_rot_tc_kernel(const __grid_constant__ QuantizeArgs a,
                 break;
             }
             tc::fence_after_sync();
-            const int64_t row = tile_of(k) * kWtRows + r;
-            const bool valid = row < a.n_rows;       // rows past the end arrive as zeros
+            int64_t row = tile_of(k) * kWtRows + r;
+            bool valid = row < a.n_rows;             // rows past the end arrive as zeros
+            if constexpr (PAGED) {
+                if (valid) {
+                    row = paged_row(a, row, status);
+                    valid = row >= 0;
+                }
+            }
             uint32_t * dst = a.codes + row * RW + half * CW;
             uint32_t words[CW];
             uint16_t nh[NBO];
@@ -1716,10 +1743,12 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }
 
 
-template <int D, int BITS, bool DENSE, bool GROUPED = false>
+template <int D, int BITS, bool DENSE, bool GROUPED = false, bool PAGED = false>
 int launch_rot_tc_t(const WhtKernelSigns & sg, const SearchTable & tabp, const QuantizeArgs & a,
                     cudaStream_t st) {
-    if constexpr (!GROUPED) {
+    if constexpr (!GROUPED && !PAGED) {
+        // the slot map of tq_quantize_kv_paged (default code order)
+        if (a.slots != nullptr) return launch_rot_tc_t<D, BITS, DENSE, false, true>(sg, tabp, a, st);
         // lane-grouped rows: d = 128 only (the caller checks)
         if (a.grouped) {
             if constexpr (D == 128) return launch_rot_tc_t<D, BITS, DENSE, true>(sg, tabp, a, st);
@@ -1727,7 +1756,7 @@ int launch_rot_tc_t(const WhtKernelSigns & sg, const SearchTable & tabp, const Q
         }
     }
     using C = WtCfg<D, BITS, DENSE>;
-    auto k = quantize_rot_tc_kernel<D, BITS, DENSE, GROUPED>;
+    auto k = quantize_rot_tc_kernel<D, BITS, DENSE, GROUPED, PAGED>;
     const int64_t n_tiles = (a.n_rows + kWtRows - 1) / kWtRows;
     if (n_tiles == 0) return 0;
     // [n_rows][D] bf16, boxes of 64 columns x 128 rows, 128-byte swizzle
@@ -1880,6 +1909,20 @@ bool encode_tensor_map_2d(CUtensorMap * map, CUtensorMapDataType dtype, const vo
     const cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer};
     const cuuint32_t estride[2] = {1u, 1u};
     return enc(map, dtype, 2, const_cast<void *>(base), gdim, gstride, box, estride,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_tensor_map_3d(CUtensorMap * map, CUtensorMapDataType dtype, const void * base,
+                          const uint64_t * dims, const uint64_t * strides, const uint32_t * box,
+                          CUtensorMapSwizzle swizzle) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (enc == nullptr) return false;
+    const cuuint64_t gdim[3] = {dims[0], dims[1], dims[2]};
+    const cuuint64_t gstride[2] = {strides[0], strides[1]};
+    const cuuint32_t gbox[3] = {box[0], box[1], box[2]};
+    const cuuint32_t estride[3] = {1u, 1u, 1u};
+    return enc(map, dtype, 3, const_cast<void *>(base), gdim, gstride, gbox, estride,
                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -161,6 +161,15 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst_saddr, const void * tma
         :: "r"(dst_saddr), "l"(tmap), "r"(x), "r"(y), "r"(bar_saddr) : "memory");
 }
 
+// The same for a tensor map of three dimensions.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst_saddr, const void * tmap, int32_t x,
+                                            int32_t y, int32_t z, uint32_t bar_saddr) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];"
+        :: "r"(dst_saddr), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar_saddr) : "memory");
+}
+
 // Bulk copy (no tensor map, no multicast) of `bytes` from global to shared
 // memory, completing on mbarrier `bar`; both addresses 16-byte aligned, bytes
 // a multiple of 16.

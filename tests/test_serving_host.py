@@ -1,0 +1,151 @@
+"""CPU tests of the serving entry points: every refusal comes before a launch
+(fake device pointers are never dereferenced), and the Python layer refuses
+tensors whose type, shape or layout the kernels would misread."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+import kv_cache_vector_11_b200 as tq
+from kv_cache_vector_11_b200 import _lib
+
+torch = pytest.importorskip("torch")
+
+FAKE = 1 << 20
+OK, INVALID, UNSUPPORTED = 0, 1, 2
+L = _lib._lib
+
+
+@pytest.fixture(scope="module")
+def rot():
+    return tq.Rotation("wht", 128, 128, 1000)
+
+
+def tables(ctx=FAKE, new=FAKE, batch=4, page=16, n_pages=8, free=FAKE, n_free=8, table=FAKE, max_pages=4, cu=FAKE,
+           total=FAKE + 4096, slots=FAKE, pos=FAKE, n_slots=16, taken=FAKE, status=None):
+    return L.tq_page_tables(ctx, new, batch, page, n_pages, free, n_free, table, max_pages, cu, total, slots, pos,
+                            n_slots, taken, status, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=0), INVALID), (dict(batch=16385), UNSUPPORTED), (dict(page=24), UNSUPPORTED),
+    (dict(page=8), UNSUPPORTED), (dict(page=1 << 17), UNSUPPORTED), (dict(n_pages=0), INVALID),
+    (dict(max_pages=0), INVALID), (dict(n_free=-1), INVALID), (dict(n_slots=-1), INVALID), (dict(ctx=None), INVALID),
+    (dict(new=None), INVALID), (dict(table=None), INVALID), (dict(cu=None), INVALID), (dict(total=None), INVALID),
+    (dict(taken=None), INVALID), (dict(free=None), INVALID), (dict(slots=None), INVALID),
+    (dict(total=FAKE), INVALID), (dict(slots=FAKE + 4), INVALID), (dict(cu=FAKE + 2), INVALID),
+])
+def test_page_tables_refusals(kw, code):
+    assert tables(**kw) == code and tq.TQError(code, "x").args
+
+
+def paged(rot, bits=4, block=32, x=FAKE, dtype=1, n=4, heads=2, d=128, slots=FAKE, page=16, n_pages=8, codes=FAKE,
+          norms=FAKE, c=None, t=None):
+    kc, kt = tq.build_codebook(max(bits, 1), 32)
+    return L.tq_quantize_kv_paged(rot.handle, bits, block, kc.ctypes.data, kt.ctypes.data, x, dtype, n, heads, d, slots,
+                                  page, n_pages, codes, norms, None, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(bits=1), UNSUPPORTED), (dict(block=64), UNSUPPORTED), (dict(dtype=2), INVALID), (dict(n=-1), INVALID),
+    (dict(heads=0), INVALID), (dict(n=1 << 30, heads=4), UNSUPPORTED), (dict(d=64), INVALID),
+    (dict(page=17), UNSUPPORTED), (dict(n_pages=0), INVALID), (dict(x=None), INVALID), (dict(slots=None), INVALID),
+    (dict(codes=None), INVALID), (dict(norms=None), INVALID), (dict(x=FAKE + 8), INVALID),
+    (dict(slots=FAKE + 4), INVALID), (dict(norms=FAKE + 8), INVALID), (dict(n=0, x=None), OK),
+])
+def test_quantize_paged_refusals(rot, kw, code):
+    assert paged(rot, **kw) == code
+
+
+def prompt(q=FAKE, k=FAKE, v=FAKE, dtype=1, cu_q=FAKE, cu_k=None, batch=2, tq_=8, tk=8, hq=4, hk=2, d=128, qs=512,
+           ks=256, vs=256, scale=0.0, out=FAKE):
+    return L.tq_prompt_attention(q, k, v, dtype, cu_q, cu_k, batch, tq_, tk, hq, hk, d, qs, ks, vs, scale, out, None,
+                                 None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(d=96), UNSUPPORTED), (dict(dtype=0), UNSUPPORTED), (dict(dtype=7), UNSUPPORTED), (dict(hq=3), INVALID),
+    (dict(hk=0), INVALID), (dict(batch=0), INVALID), (dict(tq_=-1), INVALID), (dict(tq_=1 << 31), UNSUPPORTED),
+    (dict(qs=511), INVALID), (dict(qs=504), INVALID), (dict(ks=248), INVALID), (dict(vs=260), INVALID),
+    (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(out=None), INVALID), (dict(cu_q=None), INVALID),
+    (dict(q=FAKE + 8), INVALID), (dict(out=FAKE + 8), INVALID), (dict(cu_k=FAKE + 2), INVALID),
+    (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(tq_=0, q=None), OK),
+])
+def test_prompt_refusals(kw, code):
+    assert prompt(**kw) == code
+
+
+def tree(rot, kb=4, vb=3, block=32, q=FAKE, dtype=1, cu=FAKE, batch=2, rows=8, nodes=4, lens=FAKE, max_len=64,
+         mask=FAKE, words=1, hq=4, hk=2, d=128, page=16, n_pages=8, table=FAKE, max_pages=4, kc=FAKE, kn=FAKE, vc=FAKE,
+         vn=FAKE, scale=0.0, out=FAKE, ws=FAKE, ws_bytes=1 << 40):
+    c = [tq.build_codebook(max(b, 1), 32)[0] for b in (kb, vb)]
+    return L.tq_tree_attention(rot.handle, kb, vb, block, c[0].ctypes.data, c[1].ctypes.data, q, dtype, cu, batch, rows,
+                               nodes, lens, max_len, mask, words, hq, hk, d, page, n_pages, table, max_pages, kc, kn, vc,
+                               vn, scale, out, ws, ws_bytes, None, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(kb=1), UNSUPPORTED), (dict(vb=1), UNSUPPORTED), (dict(block=64), UNSUPPORTED), (dict(dtype=3), INVALID),
+    (dict(d=64), INVALID), (dict(batch=0), INVALID), (dict(rows=-1), INVALID), (dict(nodes=0), INVALID),
+    (dict(nodes=257, words=5), INVALID), (dict(nodes=65, words=1), INVALID), (dict(hq=5), INVALID),
+    (dict(hk=0), INVALID), (dict(page=20), UNSUPPORTED), (dict(n_pages=0), INVALID), (dict(max_len=65), INVALID),
+    (dict(q=None), INVALID), (dict(cu=None), INVALID), (dict(lens=None), INVALID), (dict(table=None), INVALID),
+    (dict(kc=None), INVALID), (dict(vn=None), INVALID), (dict(out=None), INVALID), (dict(ws=None), INVALID),
+    (dict(ws_bytes=0), INVALID), (dict(ws=FAKE + 128), INVALID), (dict(q=FAKE + 8), INVALID),
+    (dict(vc=FAKE + 4), INVALID), (dict(mask=FAKE + 4), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(rows=0, q=None), OK),
+])
+def test_tree_refusals(rot, kw, code):
+    assert tree(rot, **kw) == code
+
+
+def test_tree_workspace_is_zero_for_refused_sizes_and_monotone():
+    size = tq.tree_workspace_size
+    assert size(0, 8, 4, 4, 2, 64, 128) == 0 and size(2, 8, 257, 4, 2, 64, 128) == 0
+    assert size(2, 8, 4, 5, 2, 64, 128) == 0 and size(2, 8, 4, 4, 2, 64, 96) == 0
+    small = size(2, 8, 4, 4, 2, 64, 128)
+    assert small > 0
+    assert size(2, 8, 4, 4, 2, 4096, 128) >= small and size(2, 16, 8, 4, 2, 64, 128) >= small
+
+
+def _i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def test_python_refuses_misread_tensors(rot):
+    q = torch.zeros((4, 4, 128), dtype=torch.bfloat16)
+    k = torch.zeros((4, 2, 128), dtype=torch.bfloat16)
+    cu = _i32(3)
+    for bad in (dict(cu_q=cu.long()), dict(q=q.half()), dict(k=k[:, :, ::2]), dict(v=k[:3]), dict(cu_k=_i32(4)),
+                dict(out=q.float()), dict(out=q.transpose(0, 1).contiguous().transpose(0, 1))):
+        kw = dict(q=q, k=k, v=k, cu_q=cu)
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            tq.prompt_attention(kw.pop("q"), kw.pop("k"), kw.pop("v"), kw.pop("cu_q"), **kw)
+    with pytest.raises(ValueError):                     # another number of keys needs offsets of its own
+        tq.prompt_attention(q, torch.zeros((5, 2, 128), dtype=torch.bfloat16),
+                            torch.zeros((5, 2, 128), dtype=torch.bfloat16), cu)
+    for bad in (dict(ctx=_i32(2).long()), dict(new=_i32(3)), dict(table=_i32(3, 2)), dict(table=_i32(2, 4)[:, ::2])):
+        kw = dict(ctx=_i32(2), new=_i32(2), table=_i32(2, 2))
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            tq.page_tables(kw["ctx"], kw["new"], 16, 4, _i32(4), kw["table"], 8)
+    x = torch.zeros((4, 2, 128), dtype=torch.bfloat16)
+    kc, kt = tq.build_codebook(4)
+    slots, codes, norms = torch.zeros(4, dtype=torch.int64), _i32(3, 2, 16, 16), torch.zeros((3, 2, 16, 4), dtype=torch.int16)
+    for bad in (dict(slots=slots.int()), dict(codes=_i32(3, 2, 16, 12)), dict(norms=norms.half()), dict(x=x[:, :1]),
+                dict(codes=_i32(3, 1, 16, 16))):
+        kw = dict(x=x, slots=slots, codes=codes, norms=norms)
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            tq.quantize_kv_paged(rot, 4, kc, kt, kw["x"], kw["slots"], kw["codes"], kw["norms"], 16)
+    pages = dict(k_codes=codes, k_norms=norms, v_codes=_i32(3, 2, 16, 12), v_norms=norms)
+    mask = torch.zeros((4, 1), dtype=torch.int64)
+    for bad in (dict(cu=_i32(2)), dict(lens=_i32(2).long()), dict(mask=mask.int()), dict(mask=mask[:3]),
+                dict(pages=dict(pages, v_codes=codes)), dict(q=q[:, ::2]), dict(table=_i32(3, 4))):
+        kw = dict(q=q, cu=_i32(3), lens=_i32(2), pages=pages, table=_i32(2, 4), mask=mask)
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            tq.tree_attention(rot, 4, 3, kc, tq.build_codebook(3)[0], kw["q"], kw["cu"], kw["lens"], kw["pages"],
+                              kw["table"], 16, 2, 64, tree_mask=kw["mask"])
