@@ -1,6 +1,30 @@
 // Causal attention of packed sequences over their unquantized keys and values
-// (tq_prompt_attention): one warp per (query, head), online softmax in fp32.
+// (tq_prompt_attention), on the tensor cores.
+//
+//   o_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = 2^(mul <q_i, k_j> - ref_i),   j <= i + nk - nq
+//
+// A CTA takes one or two tiles of 128 rows of one sequence and one KV head.  A
+// row is a (query, head of the group) pair, heads inner, so a tile holds
+// 128 / GP consecutive queries: grouped heads share every key tile that is
+// loaded, and the tiles cut by the causal edge are GP times fewer.  Key and
+// value tiles (128 keys) arrive by TMA into one ring of buffers, from the last
+// key tile to the first; one thread issues the MMAs, one softmax thread per row
+// reads its scores from TMEM and writes the weights back over them (tq_fmha.cuh).
+//
+//  d <= 128: two row tiles; the tensor core works on one tile while the
+//    softmax warps of the other run, and the pair shares the key ring.
+//  d = 256: one row tile (its accumulator fills half of TMEM); the scores of
+//    key tile j + 1 are computed into the second slot during the softmax of j.
+//    The head dimension is cut into halves of 128 columns, one buffer each.
+//
+// Values at keys that a row may not attend meet a zero weight, which a NaN or
+// an infinity would turn into NaN.  Such pairs exist only in the tiles at the
+// causal edge and at the sequence's end.  There two warps look over the value
+// tile before the second product: rows past the sequence are zeroed, and a
+// non-finite value inside it makes the CTA compute its rows again on the CUDA
+// cores, with the keys that a row attends and no others.
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -8,13 +32,17 @@
 
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "tq_device.cuh"
+#include "tq_fmha.cuh"
 
 namespace tq {
 namespace {
 
-constexpr int kPaThreads = 128;
+using fm::kTile;
+
+constexpr int kPaMaxHeads = 32;      // heads of a group in one row tile
 
 struct PromptArgs {
     const void * q;
@@ -26,9 +54,30 @@ struct PromptArgs {
     int64_t total_q, total_k;
     int32_t n_q_heads, n_kv_heads;
     int64_t q_stride, k_stride, v_stride;
+    int32_t heads, queries;          // GP; queries of a row tile (128 / GP)
     float scale;
     void * out;
     uint32_t * status;
+};
+
+template <int D>
+struct PaCfg {
+    static constexpr int NQ = D == 256 ? 1 : 2;          // row tiles of a CTA
+    static constexpr int NH = D == 256 ? 2 : 1;          // buffers of a key or value tile
+    static constexpr int W = D / NH;                     // columns of a buffer
+    static constexpr int SLICE = kTile * 128;            // 64 columns of 128 rows
+    static constexpr int BUF = W / 64 * SLICE;
+    static constexpr int STAGES = D == 64 ? 8 : 5;
+    static constexpr int THREADS = 128 * NQ + 128;
+    static constexpr int OFF_KV = NQ * NH * BUF;
+    static constexpr int OFF_BAR = OFF_KV + STAGES * BUF;
+    // mbarriers: q, full[STAGES], empty[STAGES], s_full[2], p_full[2],
+    // o_done[2], scanned, drained; then the TMEM address, error and redo flags, the
+    // tile, and the sums of the search for it
+    static constexpr int N_BAR = 2 * STAGES + 9;
+    static constexpr int OFF_MISC = OFF_BAR + 8 * N_BAR;
+    static constexpr int SMEM = OFF_MISC + 32 + 8 * (THREADS / 32) + 1024;   // + alignment of the base
+    static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -38,27 +87,17 @@ __device__ __forceinline__ void from_f32(float x, __half * o) { *o = __float2hal
 
 __device__ __forceinline__ int64_t clamp_to(int64_t x, int64_t lo, int64_t hi) { return min(max(x, lo), hi); }
 
+// One row by one warp on the CUDA cores: the first n keys from row k0 on.
 template <int D, typename T>
-__global__ void __launch_bounds__(kPaThreads) prompt_simple_kernel(const __grid_constant__ PromptArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * (kPaThreads / 32) + (threadIdx.x >> 5);
-    const int64_t tok = w / a.n_q_heads;
-    const int h = (int)(w % a.n_q_heads);
-    if (tok >= a.total_q) return;
-    int lo = 0, hi = a.batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu_q[mid] <= tok) lo = mid; else hi = mid;
-    }
-    const int64_t q0 = clamp_to(a.cu_q[lo], 0, a.total_q), q1 = clamp_to(a.cu_q[lo + 1], q0, a.total_q);
-    if (tok < q0 || tok >= q1) return;
-    const int64_t k0 = clamp_to(a.cu_k[lo], 0, a.total_k), k1 = clamp_to(a.cu_k[lo + 1], k0, a.total_k);
-    const int64_t n = clamp_to(tok - q0 + (k1 - k0) - (q1 - q0) + 1, 0, k1 - k0);
-    const int hk = h / (a.n_q_heads / a.n_kv_heads);
+__device__ __noinline__ void prompt_row(const PromptArgs & a, int64_t tok, int h, int hk, int64_t k0, int64_t n) {
     constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
     float q[E], o[E];
     const T * qp = static_cast<const T *>(a.q) + tok * a.q_stride + (int64_t)h * D;
-    for (int e = 0; e < E; ++e) { q[e] = to_f32(qp[lane + 32 * e]) * a.scale; o[e] = 0.0f; }
+    for (int e = 0; e < E; ++e) {
+        q[e] = to_f32(qp[lane + 32 * e]) * a.scale;
+        o[e] = 0.0f;
+    }
     float m = -CUDART_INF_F, l = 0.0f;
     for (int64_t j = k0; j < k0 + n; ++j) {
         const T * kp = static_cast<const T *>(a.k) + j * a.k_stride + (int64_t)hk * D;
@@ -76,16 +115,390 @@ __global__ void __launch_bounds__(kPaThreads) prompt_simple_kernel(const __grid_
     for (int e = 0; e < E; ++e) from_f32(n > 0 ? o[e] / l : 0.0f, op + lane + 32 * e);
 }
 
-template <int D, typename T>
-int launch_prompt_t(const PromptArgs & a, cudaStream_t st) {
-    const int64_t warps = a.total_q * a.n_q_heads, per = kPaThreads / 32;
-    prompt_simple_kernel<D, T><<<(unsigned)((warps + per - 1) / per), kPaThreads, 0, st>>>(a);
-    return (int)cudaGetLastError();
+template <int D, bool BF16>
+__global__ void __launch_bounds__(PaCfg<D>::THREADS, 1)
+prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap qmap,
+              const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using C = PaCfg<D>;
+    using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+    constexpr int NQ = C::NQ, NH = C::NH, SW = C::W / 64, ST = C::STAGES, NT = C::THREADS;
+    extern __shared__ unsigned char smem_raw[];
+    // the swizzled tiles need 1024-byte alignment
+    const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    unsigned char * smem = smem_raw + (sbase - raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t bar = sbase + (uint32_t)C::OFF_BAR;
+    const uint32_t q_full = bar, full = bar + 8u, empty = full + 8u * ST, s_full = empty + 8u * ST,
+                   p_full = s_full + 16u, o_done = p_full + 16u, scanned = o_done + 16u, drained = scanned + 8u;
+    uint32_t * s_tmem = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+    volatile int * s_err = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+    volatile int * s_redo = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8);
+    int * s_seq = reinterpret_cast<int *>(smem + C::OFF_MISC + 12);      // sequence, tile
+    int64_t * s_sums = reinterpret_cast<int64_t *>(smem + C::OFF_MISC + 32);
+
+    // which sequence and tile: the tiles of all sequences are counted one
+    // sequence after another; blocks of one tile and all heads follow each other
+    const int n_groups = a.n_q_heads / a.heads;
+    const int64_t tau = blockIdx.x / (unsigned)n_groups;
+    const int hg = (int)(blockIdx.x - (unsigned)tau * (unsigned)n_groups);
+    const int cta_queries = NQ * a.queries;
+    if (tid == 0) {
+        s_seq[0] = -1;
+        *s_err = 0;
+        *s_redo = 0;
+    }
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += NT) {
+        const int b = b0 + tid;
+        int64_t n = 0;
+        if (b < a.batch) {
+            const int64_t r0 = clamp_to(a.cu_q[b], 0, a.total_q), r1 = clamp_to(a.cu_q[b + 1], r0, a.total_q);
+            n = (r1 - r0 + cta_queries - 1) / cta_queries;
+        }
+        int64_t incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        __syncthreads();
+        if (lane == 31) s_sums[warp] = incl;
+        __syncthreads();
+        int64_t all = 0;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            const int64_t s = s_sums[w];
+            if (w < warp) incl += s;
+            all += s;
+        }
+        incl += before;
+        if (tau < incl && tau >= incl - n) {
+            s_seq[0] = b;
+            s_seq[1] = (int)(incl - 1 - tau);            // the last tile first: it has the most keys
+        }
+        before += all;
+        if (before > tau) break;
+    }
+    __syncthreads();
+    const int seq = s_seq[0];
+    if (seq < 0) return;                                  // past the last tile
+    const int64_t q0 = clamp_to(a.cu_q[seq], 0, a.total_q), q1 = clamp_to(a.cu_q[seq + 1], q0, a.total_q);
+    const int64_t k0 = clamp_to(a.cu_k[seq], 0, a.total_k), k1 = clamp_to(a.cu_k[seq + 1], k0, a.total_k);
+    const int nq = (int)(q1 - q0), nk = (int)(k1 - k0);
+    const int i0 = s_seq[1] * cta_queries;                // first query of this CTA
+    const int shift = nk - nq;                            // query i attends the keys below i + shift + 1
+    const int i_last = min(i0 + cta_queries, nq) - 1;
+    const int n_keys = max(i_last + shift + 1, 0);        // (at most nk)
+    const int n = (n_keys + kTile - 1) / kTile;           // key tiles, taken from the last to the first
+    const int full_keys = min(max(i0 + shift + 1, 0), nk);    // keys that every row attends
+    const int n_edge = n - full_keys / kTile;             // tiles with a key that some row does not attend
+    const int slots = NQ == 2 && i0 + a.queries < nq ? 2 : 1;
+    const int h0 = hg * a.heads, hk = h0 / (a.n_q_heads / a.n_kv_heads);
+
+    if (n > 0) {
+        if (tid == 0) {
+            tc::mbar_init(q_full, 1);
+            for (int i = 0; i < ST; ++i) {
+                tc::mbar_init(full + 8u * i, 1);
+                tc::mbar_init(empty + 8u * i, 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                tc::mbar_init(s_full + 8u * i, 1);
+                tc::mbar_init(p_full + 8u * i, 128);
+                tc::mbar_init(o_done + 8u * i, 1);
+            }
+            tc::mbar_init(scanned, 64);
+            tc::mbar_init(drained, 1);
+        }
+        if (warp == 0) tc::tmem_alloc(sbase + (uint32_t)C::OFF_MISC, 512);
+        tc::fence_before_sync();
+        __syncthreads();
+        tc::fence_after_sync();
+    }
+    const uint32_t tmem = n > 0 ? *s_tmem : 0u;
+    const int ctrl = warp - 4 * NQ;                       // 0: MMAs, 1: copies, 2 and 3: value scan
+
+    if (n > 0 && ctrl == 1) {
+        if (lane == 0) {
+            // queries: boxes of 64 columns, GP heads, 128 / GP tokens
+            const uint32_t rows = (uint32_t)(a.heads * a.queries);
+            tc::mbar_arrive_expect_tx(q_full, (uint32_t)slots * (D / 64) * rows * 128u);
+            for (int i = 0; i < slots; ++i)
+                for (int c = 0; c < D / 64; ++c)
+                    tc::tma_load_3d(sbase + (uint32_t)((i * (D / 64) + c) * C::SLICE), &qmap, 64 * c, h0,
+                                    (int)(q0 + i0 + i * a.queries), q_full);
+            int it = 0;
+            bool ok = true;
+            for (int j = 0; j < n && ok; ++j) {
+                const int key = (int)k0 + (n - 1 - j) * kTile;
+#pragma unroll 1
+                for (int kv = 0; kv < 2 && ok; ++kv) {
+                    const CUtensorMap * map = kv == 0 ? &kmap : &vmap;
+#pragma unroll 1
+                    for (int h = 0; h < NH && ok; ++h, ++it) {
+                        const int s = it % ST;
+                        if (it >= ST) ok = tc::mbar_wait(empty + 8u * s, (uint32_t)((it / ST - 1) & 1), fm::kWaitNs) && *s_err == 0;
+                        if (!ok) break;
+                        tc::mbar_arrive_expect_tx(full + 8u * s, (uint32_t)C::BUF);
+                        for (int c = 0; c < SW; ++c)
+                            tc::tma_load_3d(sbase + (uint32_t)(C::OFF_KV + s * C::BUF + c * C::SLICE), map,
+                                            64 * (h * SW + c), hk, key, full + 8u * s);
+                    }
+                }
+            }
+            if (!ok) *s_err = 1;
+            // the last copy into every buffer lands before the CTA ends
+            tc::mbar_wait(q_full, 0u, fm::kWaitNs);
+            for (int t = max(0, it - ST); t < it; ++t)
+                tc::mbar_wait(full + 8u * (t % ST), (uint32_t)((t / ST) & 1), fm::kWaitNs);
+        }
+        __syncwarp();
+    } else if (n > 0 && ctrl == 0) {
+        if (lane == 0) {
+            constexpr uint32_t id_qk = fm::idesc(BF16, kTile, false), id_pv = fm::idesc(BF16, C::W, true);
+            bool ok = tc::mbar_wait(q_full, 0u, fm::kWaitNs);
+            auto wait_buf = [&](int it) {
+                return tc::mbar_wait(full + 8u * (it % ST), (uint32_t)((it / ST) & 1), fm::kWaitNs) && *s_err == 0;
+            };
+            auto buf = [&](int it) { return sbase + (uint32_t)(C::OFF_KV + (it % ST) * C::BUF); };
+            // scores of row tile i and the key half h at `it` into slot s
+            auto qk = [&](int i, int s, int h, int it) {
+                const uint32_t qa = sbase + (uint32_t)((i * NH + h) * C::BUF), kb = buf(it);
+#pragma unroll
+                for (int ks = 0; ks < C::W / 16; ++ks) {
+                    const uint32_t off = (uint32_t)((ks >> 2) * C::SLICE + (ks & 3) * 32);
+                    tc::mma_bf16(tmem + (uint32_t)s * fm::kSlotCols, tc::smem_desc_sw128(qa + off),
+                                 tc::smem_desc_sw128(kb + off), id_qk, h > 0 || ks > 0 ? 1u : 0u);
+                }
+            };
+            // weights in slot s times the value half h at `it` onto accumulator i
+            auto pv = [&](int i, int s, int h, int it, bool acc) {
+                const uint32_t vb = buf(it);
+#pragma unroll
+                for (int ks = 0; ks < kTile / 16; ++ks)
+                    fm::mma_ts(tmem + fm::kOutCol + (uint32_t)(i * D + h * C::W), tmem + (uint32_t)s * fm::kSlotCols + 8u * ks,
+                               fm::smem_desc_sw128_mn(vb + 2048u * ks, (uint32_t)C::SLICE), id_pv, acc || ks > 0 ? 1u : 0u);
+            };
+            if constexpr (NQ == 2) {
+                ok = ok && wait_buf(0);
+                if (ok) {
+                    for (int i = 0; i < slots; ++i) {
+                        qk(i, i, 0, 0);
+                        tc::commit(s_full + 8u * i);
+                    }
+                    tc::commit(empty);
+                }
+                for (int j = 0; j < n && ok; ++j) {
+                    const int iv = 2 * j + 1, ik = 2 * j + 2;
+                    ok = wait_buf(iv) && (j >= n_edge || tc::mbar_wait(scanned, (uint32_t)(j & 1), fm::kWaitNs));
+                    for (int i = 0; i < slots && ok; ++i) {
+                        ok = tc::mbar_wait(p_full + 8u * i, (uint32_t)(j & 1), fm::kWaitNs) && *s_err == 0;
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        pv(i, i, 0, iv, j > 0);
+                        tc::commit(o_done + 8u * i);
+                        if (i == slots - 1) tc::commit(empty + 8u * (iv % ST));
+                        if (j + 1 < n) {
+                            if (i == 0) ok = wait_buf(ik);
+                            if (!ok) break;
+                            qk(i, i, 0, ik);
+                            tc::commit(s_full + 8u * i);
+                            if (i == slots - 1) tc::commit(empty + 8u * (ik % ST));
+                        }
+                    }
+                }
+            } else {
+                auto scores = [&](int j) {
+                    for (int h = 0; h < NH && ok; ++h) {
+                        const int it = 2 * NH * j + h;
+                        ok = wait_buf(it);
+                        if (!ok) return;
+                        tc::fence_after_sync();
+                        qk(0, j & 1, h, it);
+                        tc::commit(empty + 8u * (it % ST));
+                    }
+                    tc::commit(s_full + 8u * (j & 1));
+                };
+                if (ok) scores(0);
+                for (int j = 0; j < n && ok; ++j) {
+                    if (j + 1 < n) scores(j + 1);
+                    ok = ok && (j >= n_edge || tc::mbar_wait(scanned, (uint32_t)(j & 1), fm::kWaitNs)) &&
+                         tc::mbar_wait(p_full + 8u * (j & 1), (uint32_t)((j >> 1) & 1), fm::kWaitNs) && *s_err == 0;
+                    for (int h = 0; h < NH && ok; ++h) {
+                        const int it = 2 * NH * j + NH + h;
+                        ok = wait_buf(it);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        pv(0, j & 1, h, it, j > 0);
+                        tc::commit(empty + 8u * (it % ST));
+                    }
+                    if (ok) tc::commit(o_done);
+                }
+            }
+            if (!ok) {
+                // the MMAs in flight end before their columns are freed
+                *s_err = 1;
+                tc::commit(drained);
+                tc::mbar_wait(drained, 0u, fm::kWaitNs);
+            }
+        }
+        __syncwarp();
+    } else if (n > 0 && ctrl >= 2) {
+        // values of the edge tiles: thread t looks over rows t and t + 64
+        const int t = tid - 128 * NQ - 64;
+        bool ok = true;
+        for (int j = 0; j < n_edge && ok; ++j) {
+            bool bad = false;
+            for (int h = 0; h < NH && ok; ++h) {
+                const int it = 2 * NH * j + NH + h;
+                ok = tc::mbar_wait(full + 8u * (it % ST), (uint32_t)((it / ST) & 1), fm::kWaitNs) && *s_err == 0;
+                if (!ok) break;
+                unsigned char * vb = smem + C::OFF_KV + (it % ST) * C::BUF;
+                for (int r = t; r < kTile; r += 64) {
+                    uint32_t non = 0u;
+                    for (int c = 0; c < C::W / 8; ++c) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(vb + (c >> 3) * C::SLICE + r * 128 + 16 * ((c & 7) ^ (r & 7)));
+                        // an exponent of all ones carries into the bit above it
+                        constexpr uint32_t E = BF16 ? 0x7F807F80u : 0x7C007C00u, ONE = BF16 ? 0x00800080u : 0x04000400u;
+                        non |= ((u.x & E) + ONE) | ((u.y & E) + ONE) | ((u.z & E) + ONE) | ((u.w & E) + ONE);
+                    }
+                    if ((non & 0x80008000u) == 0u) continue;
+                    if ((n - 1 - j) * kTile + r < nk) {
+                        bad = true;
+                    } else {
+                        for (int c = 0; c < C::W / 8; ++c)
+                            *reinterpret_cast<uint4 *>(vb + (c >> 3) * C::SLICE + r * 128 + 16 * (c & 7)) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+            }
+            if (bad) *s_redo = 1;
+            // one tile ahead of the products at most: `scanned` must not pass
+            // a phase that the issuing thread has not waited for
+            if (j > 0) ok = ok && tc::mbar_wait(o_done, (uint32_t)((j - 1) & 1), fm::kWaitNs);
+            if (!ok) {
+                *s_err = 1;
+                break;
+            }
+            tc::fence_proxy_async();
+            tc::mbar_arrive(scanned);
+        }
+    } else if (ctrl < 0) {
+        const int i = warp >> 2;                          // row tile
+        const int r = tid & 127;
+        const int g = r % a.heads, qt = r / a.heads;
+        const int qi = i0 + i * a.queries + qt;
+        const bool valid = qt < a.queries && qi < nq;
+        const int lim = valid ? min(max(qi + shift + 1, 0), nk) : 0;      // keys of this row
+        T * op = static_cast<T *>(a.out) + ((q0 + qi) * a.n_q_heads + h0 + g) * D;
+        if (n > 0 && i < slots) {
+            const uint32_t lane_tm = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+            const uint32_t o_tm = lane_tm + fm::kOutCol + (uint32_t)(i * D);
+            const float mul = a.scale * 1.4426950408889634f;
+            fm::RowState st{-CUDART_INF_F, 0.0f};
+            bool ok = true;
+            for (int j = 0; j < n && ok; ++j) {
+                const int slot = NQ == 2 ? i : (j & 1), use = NQ == 2 ? j : (j >> 1);
+                ok = tc::mbar_wait(s_full + 8u * slot, (uint32_t)(use & 1), fm::kWaitNs) && *s_err == 0;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc::fence_after_sync();
+                const uint32_t s_tm = lane_tm + (uint32_t)slot * fm::kSlotCols;
+                auto wait_acc = [&] { return tc::mbar_wait(o_done + 8u * i, (uint32_t)((j - 1) & 1), fm::kWaitNs); };
+                if (j < n_edge) {
+                    const int left = lim - (n - 1 - j) * kTile;           // columns of this tile to keep
+                    uint32_t allowed[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int c = left - 32 * x;
+                        allowed[x] = c >= 32 ? 0xFFFFFFFFu : c <= 0 ? 0u : (1u << c) - 1u;
+                    }
+                    ok = fm::softmax_tile<BF16, true>(s_tm, o_tm, D, j == 0, mul, allowed, st, wait_acc);
+                } else {
+                    ok = fm::softmax_tile<BF16, false>(s_tm, o_tm, D, j == 0, mul, nullptr, st, wait_acc);
+                }
+                tc::mbar_arrive(p_full + 8u * slot);
+            }
+            ok = ok && tc::mbar_wait(o_done + 8u * i, (uint32_t)((n - 1) & 1), fm::kWaitNs);
+            if (!ok) *s_err = 1;
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+                tc::fence_after_sync();
+                const float inv = lim > 0 ? 1.0f / st.sum : 0.0f;
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    fm::tmem_ld32(o_tm + (uint32_t)c, o);
+                    if (!valid) continue;
+#pragma unroll
+                    for (int x = 0; x < 32; x += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            w[y] = lim > 0 ? fm::pack2<BF16>(__uint_as_float(o[x + 2 * y]) * inv, __uint_as_float(o[x + 2 * y + 1]) * inv) : 0u;
+                        *reinterpret_cast<uint4 *>(op + c + x) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                tc::fence_before_sync();
+            }
+        } else if (valid && n == 0) {
+            for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4 *>(op + c) = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    if (n == 0) return;
+    __syncthreads();
+    tc::fence_after_sync();
+    if (*s_err != 0 && tid == 0 && a.status != nullptr) atomicOr(a.status, TQ_STATUS_TIMEOUT);
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+    if (*s_redo != 0) {
+        __syncthreads();
+        for (int r = warp; r < NQ * a.queries * a.heads; r += NT / 32) {
+            const int qi = i0 + r / a.heads;
+            if (qi >= nq) break;
+            prompt_row<D, T>(a, q0 + qi, h0 + r % a.heads, hk, k0, min(max(qi + shift + 1, 0), nk));
+        }
+    }
+}
+
+template <int D, bool BF16>
+tq_status launch_prompt_t(PromptArgs a, cudaStream_t st) {
+    using C = PaCfg<D>;
+    // heads of a row tile: the largest divisor of the group up to 32
+    const int group = a.n_q_heads / a.n_kv_heads;
+    a.heads = 1;
+    for (int g = 2; g <= kPaMaxHeads; ++g)
+        if (group % g == 0) a.heads = g;
+    a.queries = kTile / a.heads;
+    // every sequence adds at most one tile that is not full
+    const int64_t tiles = a.total_q / ((int64_t)C::NQ * a.queries) + a.batch;
+    const int64_t grid = tiles * (a.n_q_heads / a.heads);
+    if (grid > INT32_MAX) return fail(TQ_ERR_UNSUPPORTED, "more than 2^31 - 1 row tiles");
+    CUtensorMap qmap, kmap, vmap;
+    const CUtensorMapDataType dt = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    auto encode = [&](CUtensorMap * m, const void * base, int64_t tokens, int heads, int64_t stride, int box_heads,
+                      int box_tokens) {
+        const uint64_t dims[3] = {(uint64_t)D, (uint64_t)heads, (uint64_t)tokens};
+        const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)stride * 2};
+        const uint32_t box[3] = {64u, (uint32_t)box_heads, (uint32_t)box_tokens};
+        return encode_tensor_map_3d(m, dt, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    bool ok = encode(&qmap, a.q, a.total_q, a.n_q_heads, a.q_stride, a.heads, a.queries);
+    if (a.total_k > 0) {
+        ok = ok && encode(&kmap, a.k, a.total_k, a.n_kv_heads, a.k_stride, 1, kTile) &&
+             encode(&vmap, a.v, a.total_k, a.n_kv_heads, a.v_stride, 1, kTile);
+    } else {
+        kmap = vmap = qmap;                  // (no tile is read)
+    }
+    if (!ok) return fail(TQ_ERR_UNSUPPORTED, "tensor maps of q, k and v rejected (token stride too large?)");
+    auto k = prompt_kernel<D, BF16>;
+    if (int e = ensure_dynamic_smem(reinterpret_cast<const void *>(k), C::SMEM))
+        return cuda_status(e, "prompt attention shared memory");
+    k<<<(unsigned)grid, C::THREADS, C::SMEM, st>>>(a, qmap, kmap, vmap);
+    return cuda_status((int)cudaGetLastError(), "prompt attention launch");
 }
 
 template <int D>
-int launch_prompt(const PromptArgs & a, tq_dtype dtype, cudaStream_t st) {
-    return dtype == TQ_DTYPE_BF16 ? launch_prompt_t<D, __nv_bfloat16>(a, st) : launch_prompt_t<D, __half>(a, st);
+tq_status launch_prompt(const PromptArgs & a, tq_dtype dtype, cudaStream_t st) {
+    return dtype == TQ_DTYPE_BF16 ? launch_prompt_t<D, true>(a, st) : launch_prompt_t<D, false>(a, st);
 }
 
 }  // namespace
@@ -137,7 +550,6 @@ extern "C" tq_status tq_prompt_attention(const void * q, const void * k, const v
     a.out = out;
     a.status = status_dev;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int e = head_dim == 64 ? launch_prompt<64>(a, dtype, st)
-                : head_dim == 128 ? launch_prompt<128>(a, dtype, st) : launch_prompt<256>(a, dtype, st);
-    return cuda_status(e, "prompt attention launch");
+    return head_dim == 64 ? launch_prompt<64>(a, dtype, st)
+         : head_dim == 128 ? launch_prompt<128>(a, dtype, st) : launch_prompt<256>(a, dtype, st);
 }
