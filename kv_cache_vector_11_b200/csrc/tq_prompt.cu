@@ -419,6 +419,10 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                 }
                 tc::mbar_arrive(p_full + 8u * slot);
             }
+            // the last product (d = 256: the scores of a tile come before the
+            // products of the one in front of it, so that one is waited for first:
+            // a wait may be one phase ahead of the barrier, not two)
+            if (NQ == 1 && n > 1) ok = ok && tc::mbar_wait(o_done, (uint32_t)(n & 1), fm::kWaitNs);
             ok = ok && tc::mbar_wait(o_done + 8u * i, (uint32_t)((n - 1) & 1), fm::kWaitNs);
             if (!ok) *s_err = 1;
             ok = __all_sync(0xffffffffu, ok);

@@ -1,6 +1,40 @@
 // Attention of the newest tokens of every request over its paged, packed cache
-// (tq_tree_attention): one CTA per (node, head), online softmax in fp32.
+// (tq_tree_attention), on the tensor cores.
+//
+//   out = R^T sum_t p_t v^_t / sum_t p_t,   p_t = 2^(mul <q~, k^_t> - ref),   q~ = R q
+//
+// Three launches: the queries are rotated into fp16 rows (tree_prep_kernel),
+// every CTA takes an equal share of the key tiles of all requests
+// (tree_kernel), and the shares of a row are merged and rotated back
+// (tree_combine_kernel).
+//
+// A row is a (node, head of the group) pair, heads inner; the rows of one
+// request and KV head attend the same cached tokens, so a tile of 128 keys is
+// unpacked once for all of them.  The unit of work is one key tile against one
+// set of rows, counted request by request; the grid is one CTA per SM and CTA c
+// takes the units [c W / C, (c + 1) W / C): long caches are split over many
+// CTAs, short ones share one.  Where a CTA's range starts inside a set's tiles
+// it writes its part of the sum into a slot of its own, all other parts go to
+// the rows' own slots, so a row has one own slot and one more per further CTA.
+//
+// In the CTA four warps unpack codes into the swizzled operand tiles (shared
+// memory, a ring of buffers), one thread issues the MMAs, one softmax thread
+// per row turns scores into weights (tq_fmha.cuh).  Which rows share a CTA:
+//   PAIR:   two row tiles (256 rows) against the same key tile: unpacking is
+//           paid once for both, the tensor core works on one while the softmax
+//           warps of the other run;
+//   STREAM: one row tile (at most 128 rows), the even key tiles and the odd
+//           ones with a softmax and an accumulator each: half the unpacking is
+//           hidden behind twice the softmax throughput.  Taken when no request
+//           can have more than 128 rows;
+//   WIDE:   d = 256, one row tile whose accumulator fills half of TMEM, the
+//           scores of the next key tile under way during a softmax.
+//
+// Unpacking: centroids are 16-bit table entries, looked up four at a time with
+// byte permutes (a table of 8 bytes in two registers; the low and the high
+// bytes of four entries, interleaved), times the block's norm in fp16.
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -10,12 +44,17 @@
 #include <cmath>
 
 #include "tq_device.cuh"
+#include "tq_fmha.cuh"
 
 namespace tq {
 namespace {
 
-constexpr int kTaThreads = 128;
+using fm::kTile;
+
 constexpr int kTaMaxNodes = 256;
+constexpr int kTaAhead = 4;          // key tiles fetched into L2 ahead of their unpacking
+
+enum TreeMode { PAIR = 0, STREAM = 1, WIDE = 2 };
 
 struct TreeArgs {
     const void * q;
@@ -26,21 +65,98 @@ struct TreeArgs {
     int64_t max_len;
     const uint64_t * mask;
     int32_t mask_words;
-    int32_t n_q_heads, n_kv_heads;
+    int32_t n_q_heads, n_kv_heads, group;
     int32_t page_shift, n_pages, max_pages;
     const int32_t * table;
     const uint32_t * k_codes;
     const uint16_t * k_norms;
     const uint32_t * v_codes;
     const uint16_t * v_norms;
+    int32_t k_bits, v_bits;
     float scale;
     int32_t dense;              // HAAR rotation (rot_f32) instead of Walsh-Hadamard
     const float * rot_f32;
     uint32_t d1_bits[8], d2_bits[8];
-    float kc[kMaxLevels], vc[kMaxLevels];
+    // fp16 centroids: low bytes of entries 0..15 (4 words), high bytes (4 words)
+    uint32_t k_table[8], v_table[8];
     void * out;
     uint32_t * status;
+    int32_t rows_per_set;       // rows that share a CTA: 256 (PAIR) or 128
+    int32_t streams;            // own slots of a row: 2 (STREAM) or 1
+    int32_t n_ctas;
+    // workspace
+    int64_t * unit0;            // [batch + 1] units before a request
+    __half * q_rows;            // [n_rows * n_q_heads][d], by request, KV head, node, head
+    float * q_mul;              // what a row's scores are multiplied by
+    float * own;                // [n_rows * n_q_heads * 2][d] partial sums
+    float2 * own_ml;            //   their (ref, sum of weights)
+    float * more;               // [n_ctas][2 * 128][d] parts of sets that began in an earlier CTA
+    float2 * more_ml;
 };
+
+// Request b: its first row, nodes and cached tokens, clamped as the entry point says.
+struct Request {
+    int32_t r0, n, len;
+};
+__device__ __forceinline__ Request request_of(const TreeArgs & a, int b) {
+    Request q;
+    q.r0 = min(max(a.cu[b], 0), a.n_rows);
+    q.n = min(min(max(a.cu[b + 1], q.r0), a.n_rows) - q.r0, a.max_nodes);
+    q.len = (int32_t)min((int64_t)max(a.lens[b], 0), a.max_len);
+    return q;
+}
+__device__ __forceinline__ int sets_of(const TreeArgs & a, int n) {
+    return (n * a.group + a.rows_per_set - 1) / a.rows_per_set;
+}
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+// The CTAs that share the units (no more than there are), the first unit of
+// CTA c, and the CTA whose range holds unit u.
+__device__ __forceinline__ int64_t sharers(const TreeArgs & a, int64_t units) { return min((int64_t)a.n_ctas, units); }
+__device__ __forceinline__ int64_t first_unit(int64_t c, int64_t units, int64_t n) { return n > 0 ? units * min(c, n) / n : 0; }
+__device__ __forceinline__ int cta_of(int64_t u, int64_t units, int64_t n) { return (int)(((u + 1) * n - 1) / units); }
+
+// The parts of this CTA's range, one per (request, KV head, row set).
+struct Part {
+    int b, hk, set, tile0, tiles;    // key tiles [tile0, tile0 + tiles)
+    Request rq;
+    int rows;                        // rows of the set (> 0)
+    int64_t row_id;                  // of the set's first row
+};
+struct PartIter {
+    int64_t u, end;
+    int b;
+    __device__ __forceinline__ void start(const TreeArgs & a, int b0) {
+        const int64_t units = a.unit0[a.batch];
+        const int64_t n = sharers(a, units);
+        u = first_unit(blockIdx.x, units, n);
+        end = first_unit(blockIdx.x + 1, units, n);
+        b = b0;
+    }
+    __device__ __forceinline__ bool next(const TreeArgs & a, Part & p) {
+        if (u >= end) return false;
+        while (u >= a.unit0[b + 1]) ++b;
+        p.b = b;
+        p.rq = request_of(a, b);
+        const int sets = sets_of(a, p.rq.n), tiles = tiles_of(p.rq.len);
+        const int64_t rel = u - a.unit0[b];
+        const int64_t s = rel / tiles;
+        p.tile0 = (int)(rel - s * tiles);
+        p.hk = (int)(s / sets);
+        p.set = (int)(s - (int64_t)p.hk * sets);
+        p.tiles = (int)min((int64_t)(tiles - p.tile0), end - u);
+        p.rows = min(a.rows_per_set, p.rq.n * a.group - p.set * a.rows_per_set);
+        p.row_id = (int64_t)p.rq.r0 * a.n_q_heads + (int64_t)p.hk * p.rq.n * a.group + (int64_t)p.set * a.rows_per_set;
+        u += p.tiles;
+        return true;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Rotation of the queries
+// ---------------------------------------------------------------------------
+
+constexpr int kTpThreads = 256;
 
 __device__ __forceinline__ float load_el(const void * p, int dt, int64_t i) {
     if (dt == TQ_DTYPE_F32) return static_cast<const float *>(p)[i];
@@ -52,124 +168,824 @@ __device__ __forceinline__ void store_el(void * p, int dt, int64_t i, float v) {
     else if (dt == TQ_DTYPE_BF16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
     else static_cast<__half *>(p)[i] = __float2half_rn(v);
 }
-__device__ __forceinline__ float sgn(const uint32_t * bits, int i) {
-    return ((bits[i >> 5] >> (i & 31)) & 1u) ? -1.0f : 1.0f;
+__device__ __forceinline__ float signed_by(const uint32_t * bits, int i, float v) {
+    return ((bits[i >> 5] >> (i & 31)) & 1u) ? -v : v;
 }
 
-template <int D>
-__device__ void fwht(float * v) {
-    for (int h = 1; h < D; h <<= 1) {
-        __syncthreads();
-        for (int k = threadIdx.x; k < D / 2; k += kTaThreads) {
-            const int i = (k / h) * 2 * h + (k % h);
-            const float x = v[i], y = v[i + h];
-            v[i] = x + y;
-            v[i + h] = x - y;
+// Walsh-Hadamard transform of a vector held by a warp, lane l with elements
+// E l .. E l + E - 1, scaled by 1 / sqrt(32 E).
+template <int E>
+__device__ __forceinline__ void warp_fwht(float * v, int lane) {
+#pragma unroll
+    for (int h = 1; h < E; h <<= 1)
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            if ((i & h) == 0) {
+                const float x = v[i], y = v[i + h];
+                v[i] = x + y;
+                v[i + h] = x - y;
+            }
+#pragma unroll
+    for (int h = 1; h < 32; h <<= 1)
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const float o = __shfl_xor_sync(0xffffffffu, v[i], h);
+            v[i] = (lane & h) ? o - v[i] : v[i] + o;
         }
-    }
-    __syncthreads();
+    const float sc = rsqrtf(32.0f * E);
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] *= sc;
 }
 
-template <int D, int KB, int VB>
-__global__ void __launch_bounds__(kTaThreads) tree_simple_kernel(const __grid_constant__ TreeArgs a) {
-    constexpr int NB = D / 32, W = kTaThreads / 32;
-    __shared__ float raw[D], qr[D], part[W][D], ml[W][2];
-    const int row = blockIdx.x / a.n_q_heads, h = blockIdx.x % a.n_q_heads;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The request of a row: the last one that starts at or before it.
+__device__ __forceinline__ int request_of_row(const TreeArgs & a, int row) {
     int lo = 0, hi = a.batch;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (a.cu[mid] <= row) lo = mid; else hi = mid;
     }
-    const int r0 = max(a.cu[lo], 0), r1 = min(a.cu[lo + 1], a.n_rows);
-    if (row < r0 || row >= r1 || row - r0 >= a.max_nodes) return;
-    const int node = row - r0, n = min(r1 - r0, a.max_nodes);
-    const int64_t len = min((int64_t)max(a.lens[lo], 0), a.max_len);
-    const int64_t base = (int64_t)(row * (int64_t)a.n_q_heads + h) * D;
-    for (int i = threadIdx.x; i < D; i += kTaThreads) raw[i] = load_el(a.q, a.q_dtype, base + i);
-    __syncthreads();
-    if (!a.dense) {
-        for (int i = threadIdx.x; i < D; i += kTaThreads) qr[i] = raw[i] * sgn(a.d2_bits, i);
-        fwht<D>(qr);
-        for (int i = threadIdx.x; i < D; i += kTaThreads) qr[i] *= rsqrtf((float)D) * sgn(a.d1_bits, i);
-    } else {
-        for (int e = threadIdx.x; e < D; e += kTaThreads) {
-            float s = 0.0f;
-            for (int i = 0; i < D; ++i) s = fmaf(a.rot_f32[e * D + i], raw[i], s);
-            qr[e] = s;
-        }
-    }
-    __syncthreads();
-    const int hk = h / (a.n_q_heads / a.n_kv_heads);
-    const int64_t ctx0 = len - n;
-    float q[NB], o[NB];
-    for (int b = 0; b < NB; ++b) { q[b] = qr[32 * b + lane] * a.scale; o[b] = 0.0f; }
-    float m = -CUDART_INF_F, l = 0.0f;
-    for (int64_t t = warp; t < len; t += W) {
-        const int64_t j = t - ctx0;
-        if (j >= 0) {
-            if (a.mask != nullptr) {
-                if (!((a.mask[(int64_t)row * a.mask_words + (j >> 6)] >> (j & 63)) & 1u)) continue;
-            } else if (j > node) {
-                continue;
+    return lo;
+}
+
+// Block 0: the units before every request.  The others: one warp per (row,
+// head), q~ = R q times a power of two that brings the row's largest
+// coordinate into [1, 2), so that fp16 neither overflows nor loses the row;
+// q_mul carries the inverse, the softmax scale and log2 e.
+template <int D>
+__global__ void __launch_bounds__(kTpThreads) tree_prep_kernel(const __grid_constant__ TreeArgs a) {
+    constexpr int E = D / 32, NW = kTpThreads / 32;
+    __shared__ float x_s[NW][D];
+    __shared__ int64_t sums[NW];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (blockIdx.x == 0) {
+        int64_t before = 0;
+        for (int b0 = 0; b0 < a.batch; b0 += kTpThreads) {
+            const int b = b0 + tid;
+            int64_t n = 0;
+            if (b < a.batch) {
+                const Request q = request_of(a, b);
+                n = (int64_t)a.n_kv_heads * sets_of(a, q.n) * tiles_of(q.len);
             }
+            int64_t incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += u;
+            }
+            __syncthreads();
+            if (lane == 31) sums[warp] = incl;
+            __syncthreads();
+            int64_t all = 0;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                if (w < warp) incl += sums[w];
+                all += sums[w];
+            }
+            if (b < a.batch) a.unit0[b] = before + incl - n;
+            before += all;
         }
-        const int pg = min(max(a.table[(int64_t)lo * a.max_pages + (t >> a.page_shift)], 0), a.n_pages - 1);
-        const int64_t r = (((int64_t)pg * a.n_kv_heads + hk) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
-        float s = 0.0f;
-        for (int b = 0; b < NB; ++b) {
-            const uint32_t c = extract_code<KB>(a.k_codes + (r * NB + b) * KB, lane);
-            s = fmaf(q[b], a.kc[c] * half_bits_to_float(a.k_norms[r * NB + b]), s);
-        }
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        const float mn = fmaxf(m, s);
-        const float c = m == -CUDART_INF_F ? 0.0f : expf(m - mn), p = expf(s - mn);
-        m = mn;
-        l = l * c + p;
-        for (int b = 0; b < NB; ++b) {
-            const uint32_t vi = extract_code<VB>(a.v_codes + (r * NB + b) * VB, lane);
-            o[b] = o[b] * c + p * a.vc[vi] * half_bits_to_float(a.v_norms[r * NB + b]);
-        }
+        if (tid == 0) a.unit0[a.batch] = before;
+        return;
     }
-    for (int b = 0; b < NB; ++b) part[warp][32 * b + lane] = o[b];
-    if (lane == 0) { ml[warp][0] = m; ml[warp][1] = l; }
-    __syncthreads();
-    float M = -CUDART_INF_F, L = 0.0f;
-    for (int w = 0; w < W; ++w) M = fmaxf(M, ml[w][0]);
-    for (int w = 0; w < W; ++w) L += ml[w][0] == -CUDART_INF_F ? 0.0f : expf(ml[w][0] - M) * ml[w][1];
-    for (int i = threadIdx.x; i < D; i += kTaThreads) {
-        float t = 0.0f;
-        for (int w = 0; w < W; ++w) t += ml[w][0] == -CUDART_INF_F ? 0.0f : expf(ml[w][0] - M) * part[w][i];
-        raw[i] = L != 0.0f ? t / L : 0.0f;
-    }
-    __syncthreads();
-    if (!a.dense) {
-        for (int i = threadIdx.x; i < D; i += kTaThreads) raw[i] *= sgn(a.d1_bits, i);
-        fwht<D>(raw);
-        for (int i = threadIdx.x; i < D; i += kTaThreads)
-            store_el(a.out, a.q_dtype, base + i, raw[i] * rsqrtf((float)D) * sgn(a.d2_bits, i));
-    } else {
-        for (int i = threadIdx.x; i < D; i += kTaThreads) {
+    const int64_t vec = (int64_t)(blockIdx.x - 1) * NW + warp;
+    if (vec >= (int64_t)a.n_rows * a.n_q_heads) return;
+    const int row = (int)(vec / a.n_q_heads), h = (int)(vec - (int64_t)row * a.n_q_heads);
+    const Request q = request_of(a, request_of_row(a, row));
+    const int node = row - q.r0;
+    if (node < 0 || node >= q.n) return;
+    float v[E];
+    if (a.dense) {
+        for (int i = lane; i < D; i += 32) x_s[warp][i] = load_el(a.q, a.q_dtype, vec * D + i);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            const float4 * r = reinterpret_cast<const float4 *>(a.rot_f32 + (int64_t)(E * lane + k) * D);
             float s = 0.0f;
-            for (int e = 0; e < D; ++e) s = fmaf(a.rot_f32[e * D + i], raw[e], s);
-            store_el(a.out, a.q_dtype, base + i, s);
+            for (int i = 0; i < D / 4; ++i) {
+                const float4 w = __ldg(r + i), x = reinterpret_cast<const float4 *>(x_s[warp])[i];
+                s = fmaf(w.x, x.x, fmaf(w.y, x.y, fmaf(w.z, x.z, fmaf(w.w, x.w, s))));
+            }
+            v[k] = s;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < E; ++k) v[k] = signed_by(a.d2_bits, E * lane + k, load_el(a.q, a.q_dtype, vec * D + E * lane + k));
+        warp_fwht<E>(v, lane);
+#pragma unroll
+        for (int k = 0; k < E; ++k) v[k] = signed_by(a.d1_bits, E * lane + k, v[k]);
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < E; ++k) top = fmaxf(top, fabsf(v[k]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    int e = (int)(__float_as_uint(top) >> 23) - 127;
+    e = e == 128 ? 0 : max(e, -120);                     // (infinite or NaN rows stay so)
+    const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+    const int hk = h / a.group, g = h - hk * a.group;
+    const int64_t id = (int64_t)q.r0 * a.n_q_heads + (int64_t)hk * q.n * a.group + (int64_t)node * a.group + g;
+    __half * o = a.q_rows + id * D + E * lane;
+#pragma unroll
+    for (int k = 0; k < E; k += 2) *reinterpret_cast<__half2 *>(o + k) = __floats2half2_rn(v[k] * f, v[k + 1] * f);
+    if (lane == 0) a.q_mul[id] = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
+// ---------------------------------------------------------------------------
+// Unpacking
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t hmul2_u(uint32_t a, __half2 b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), b);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// 8 codes of a block (their nibbles in `x`) -> 4 fp16 pairs, times `norm`.
+// TOP: codes above 7 exist (4 bits); bit 3 of a code chooses between the
+// lookups in the lower and the upper half of the table.
+template <bool TOP>
+__device__ __forceinline__ uint4 lookup8(uint32_t x, const uint32_t * tab, __half2 norm) {
+    const uint32_t sel = TOP ? x & 0x77777777u : x, x4 = TOP ? x << 4 : 0u;
+    uint32_t o[4];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const uint32_t s = p ? sel >> 16 : sel;
+        uint32_t lo = __byte_perm(tab[0], tab[1], s), hi = __byte_perm(tab[4], tab[5], s);
+        if constexpr (TOP) {
+            uint32_t m;      // byte i: bit 3 of code i, replicated
+            if (p == 0) asm("prmt.b32 %0, %1, %2, 0xD9C8;" : "=r"(m) : "r"(x4), "r"(x));
+            else asm("prmt.b32 %0, %1, %2, 0xFBEA;" : "=r"(m) : "r"(x4), "r"(x));
+            lo = (__byte_perm(tab[2], tab[3], s) & m) | (lo & ~m);
+            hi = (__byte_perm(tab[6], tab[7], s) & m) | (hi & ~m);
+        }
+        o[2 * p] = hmul2_u(__byte_perm(lo, hi, 0x5140), norm);
+        o[2 * p + 1] = hmul2_u(__byte_perm(lo, hi, 0x7362), norm);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// One row of an operand buffer: NB blocks of BITS words, norms two to a word.
+template <int BITS, int NB>
+__device__ __forceinline__ void unpack_row(const uint32_t * w, const uint32_t * norms, const uint32_t * tab,
+                                           unsigned char * dst, int swz) {
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+        const uint32_t nn = __byte_perm(norms[blk >> 1], 0u, (blk & 1) ? 0x3232 : 0x1010);
+        const __half2 norm = *reinterpret_cast<const __half2 *>(&nn);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t x;
+            if constexpr (BITS == 4) {
+                x = w[4 * blk + k];
+            } else if constexpr (BITS == 3) {
+                // 24 bits -> 8 nibbles
+                const int bit = 24 * k, wi = 3 * blk + (bit >> 5), sh = bit & 31;
+                x = sh + 24 <= 32 ? w[wi] >> sh : __funnelshift_r(w[wi], w[wi + 1 < 3 * blk + 3 ? wi + 1 : wi], sh);
+                x = (x & 0x00000FFFu) | ((x << 4) & 0x0FFF0000u);
+                x = (x & 0x003F003Fu) | ((x << 2) & 0x3F003F00u);
+                x = (x & 0x07070707u) | ((x << 1) & 0x70707070u);
+            } else {
+                // 16 bits -> 8 nibbles
+                x = (w[2 * blk + (k >> 1)] >> (16 * (k & 1))) & 0xFFFFu;
+                x = (x | (x << 8)) & 0x00FF00FFu;
+                x = (x | (x << 4)) & 0x0F0F0F0Fu;
+                x = (x | (x << 2)) & 0x33333333u;
+            }
+            const int c = 4 * blk + k;                   // 16-byte chunk of the row
+            *reinterpret_cast<uint4 *>(dst + (c >> 3) * (kTile * 128) + 16 * ((c & 7) ^ swz)) = lookup8<BITS == 4>(x, tab, norm);
         }
     }
 }
 
-template <int D, int KB>
-int launch_tree_v(const TreeArgs & a, int vb, cudaStream_t st) {
-    const unsigned grid = (unsigned)((int64_t)a.n_rows * a.n_q_heads);
-    if (vb == 2) tree_simple_kernel<D, KB, 2><<<grid, kTaThreads, 0, st>>>(a);
-    else if (vb == 3) tree_simple_kernel<D, KB, 3><<<grid, kTaThreads, 0, st>>>(a);
-    else tree_simple_kernel<D, KB, 4><<<grid, kTaThreads, 0, st>>>(a);
+// The bits of a row's mask for 32 consecutive tokens, the first of them node j0
+// (negative: that many tokens before the nodes, which every node attends).
+__device__ __forceinline__ uint32_t mask32(const TreeArgs & a, const uint64_t * words, int node, int j0) {
+    if (j0 <= -32) return 0xFFFFFFFFu;
+    uint32_t bits;
+    if (words != nullptr) {
+        const int from = max(j0, 0), w = from >> 6;
+        if (w >= a.mask_words) return 0u;
+        uint64_t x = words[w] >> (from & 63);
+        if ((from & 63) > 32 && w + 1 < a.mask_words) x |= words[w + 1] << (64 - (from & 63));
+        bits = (uint32_t)x;
+    } else {
+        const int c = node + 1 - max(j0, 0);             // nodes 0 .. node
+        bits = c >= 32 ? 0xFFFFFFFFu : c <= 0 ? 0u : (1u << c) - 1u;
+    }
+    return j0 >= 0 ? bits : (bits << -j0) | ((1u << -j0) - 1u);
+}
+
+// ---------------------------------------------------------------------------
+// The key tiles
+// ---------------------------------------------------------------------------
+
+template <int D, int MODE>
+struct TaCfg {
+    static constexpr int WGS = MODE == WIDE ? 1 : 2;     // softmax warpgroups
+    static constexpr int NH = D == 256 ? 2 : 1;          // buffers of a key or value tile
+    static constexpr int W = D / NH;                     // columns of a buffer
+    static constexpr int NB = W / 32;                    // norm blocks of a buffer's row
+    static constexpr int SLICE = kTile * 128;            // 64 columns of 128 rows
+    static constexpr int BUF = W / 64 * SLICE;
+    static constexpr int QT = MODE == PAIR ? 2 : 1;      // row tiles
+    static constexpr int LEAD = MODE == PAIR ? 0 : 1;    // tiles that the keys are ahead of the values
+    static constexpr int OFF_RING = QT * NH * BUF;
+    static constexpr int STAGES = (224 * 1024 - OFF_RING) / BUF < 8 ? (224 * 1024 - OFF_RING) / BUF : 8;
+    static constexpr int THREADS = 128 * (WGS + 2);      // softmax, unpacking, MMAs
+    // mbarriers: full[STAGES], empty[STAGES], s_full[2], p_full[2], o_done[2],
+    // o_free[2], q_full, q_free, drained
+    static constexpr int OFF_BAR = OFF_RING + STAGES * BUF;
+    static constexpr int N_BAR = 2 * STAGES + 11;
+    static constexpr int OFF_BAD = (OFF_BAR + 8 * N_BAR + 15) / 16 * 16;    // 8 tiles x 128 bits: keys with a bad norm
+    static constexpr int OFF_MISC = OFF_BAD + 128;                           // TMEM address, error flag, first request
+    static constexpr int SMEM = OFF_MISC + 16 + 1024;                       // + alignment of the base
+    static_assert(SMEM <= 232448, "shared memory of a CTA");
+    // registers a thread: the launch's share is 128 (512 threads) or 168 (384)
+    static constexpr int R_SOFTMAX = WGS == 2 ? 184 : 240;
+    static constexpr int R_UNPACK = WGS == 2 ? 96 : 168;
+    static constexpr int R_MMA = WGS == 2 ? 48 : 96;
+    static_assert(WGS * R_SOFTMAX + R_UNPACK + R_MMA <= (WGS == 2 ? 512 : 504), "no more than the launch holds");
+};
+
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
+
+// A row's packed words of one buffer, in flight.
+template <int NB>
+struct Packed {
+    uint32_t w[4 * NB];
+    uint32_t norm[NB / 2];                           // of its blocks, two to a word
+    uint32_t other[NB / 2];                          // keys: the values' norms (read for the check alone)
+    int what;                                        // 0: keys, 1: values
+    int half;
+};
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const __grid_constant__ TreeArgs a,
+                                                                           const __grid_constant__ CUtensorMap qmap) {
+    using C = TaCfg<D, MODE>;
+    constexpr int WGS = C::WGS, NH = C::NH, NB = C::NB, ST = C::STAGES, LEAD = C::LEAD;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    unsigned char * smem = smem_raw + (sbase - raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t full = sbase + (uint32_t)C::OFF_BAR, empty = full + 8u * ST, s_full = empty + 8u * ST,
+                   p_full = s_full + 16u, o_done = p_full + 16u, o_free = o_done + 16u, q_full = o_free + 16u,
+                   q_free = q_full + 8u, drained = q_free + 8u;
+    volatile uint32_t * s_bad = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_BAD);
+    uint32_t * s_tmem = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+    volatile int * s_err = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+    int * s_first = reinterpret_cast<int *>(smem + C::OFF_MISC + 8);
+
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            tc::mbar_init(full + 8u * i, 4);
+            tc::mbar_init(empty + 8u * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(s_full + 8u * i, 1);
+            tc::mbar_init(p_full + 8u * i, 128);
+            tc::mbar_init(o_done + 8u * i, 1);
+            tc::mbar_init(o_free + 8u * i, 128);
+        }
+        tc::mbar_init(q_full, 1);
+        tc::mbar_init(q_free, 1);
+        tc::mbar_init(drained, 1);
+        *s_err = 0;
+    }
+    if (warp == 0) tc::tmem_alloc(sbase + (uint32_t)C::OFF_MISC, 512);
+    {
+        // the request of this CTA's first unit
+        const int64_t units = a.unit0[a.batch], u0 = first_unit(blockIdx.x, units, sharers(a, units));
+        for (int b = tid; b < a.batch; b += C::THREADS)
+            if (a.unit0[b] <= u0 && u0 < a.unit0[b + 1]) *s_first = b;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *s_tmem;
+    PartIter it;
+    it.start(a, *s_first);
+    Part p;
+
+    if (warp >= 4 * (WGS + 1)) {
+        // ---- MMAs ----
+        regs_down<C::R_MMA>();
+        if (warp == 4 * (WGS + 1) && lane == 0) {
+            constexpr uint32_t id_qk = fm::idesc(false, kTile, false), id_pv = fm::idesc(false, C::W, true);
+            bool ok = true;
+            int ring = 0, parts = 0, wide = 0;               // buffers, parts, (WIDE) tiles so far
+            int left[2] = {0, 0};          // finished parts of a softmax warpgroup
+            int slot_used[2] = {0, 0};                       // tiles of a score slot
+            auto wait = [&](uint32_t bar, int phase) { return tc::mbar_wait(bar, (uint32_t)(phase & 1), fm::kWaitNs) && *s_err == 0; };
+            // scores of row tile t against the next key tile, into slot s
+            auto qk = [&](int t, int s, int at) {
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    const uint32_t qa = sbase + (uint32_t)((t * NH + h) * C::BUF);
+                    const uint32_t kb = sbase + (uint32_t)(C::OFF_RING + ((at + h) % ST) * C::BUF);
+#pragma unroll
+                    for (int ks = 0; ks < C::W / 16; ++ks) {
+                        const uint32_t off = (uint32_t)((ks >> 2) * C::SLICE + (ks & 3) * 32);
+                        tc::mma_bf16(tmem + (uint32_t)s * fm::kSlotCols, tc::smem_desc_sw128(qa + off),
+                                     tc::smem_desc_sw128(kb + off), id_qk, h > 0 || ks > 0 ? 1u : 0u);
+                    }
+                }
+                tc::commit(s_full + 8u * s);
+            };
+            // weights of slot s times the value tile, onto accumulator w
+            auto pv = [&](int w, int s, int at, bool acc) {
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    const uint32_t vb = sbase + (uint32_t)(C::OFF_RING + ((at + h) % ST) * C::BUF);
+#pragma unroll
+                    for (int ks = 0; ks < kTile / 16; ++ks)
+                        fm::mma_ts(tmem + fm::kOutCol + (uint32_t)(w * D + h * C::W), tmem + (uint32_t)s * fm::kSlotCols + 8u * ks,
+                                   fm::smem_desc_sw128_mn(vb + 2048u * ks, (uint32_t)C::SLICE), id_pv, acc || ks > 0 ? 1u : 0u);
+                }
+                tc::commit(o_done + 8u * w);
+            };
+            auto wait_tile = [&](int at) {                   // its buffers are written
+                bool r = true;
+                for (int h = 0; h < NH && r; ++h) r = wait(full + 8u * ((at + h) % ST), (at + h) / ST);
+                tc::fence_after_sync();
+                return r;
+            };
+            auto release = [&](int at) {
+                for (int h = 0; h < NH; ++h) tc::commit(empty + 8u * ((at + h) % ST));
+            };
+            // softmax warpgroup w has written the weights in slot s; before the
+            // first product of a part its accumulator must have been read
+            auto wait_weights = [&](int w, int s, bool first) {
+                bool r = wait(p_full + 8u * s, slot_used[s]);
+                if (r && first && left[w] > 0) r = wait(o_free + 8u * w, left[w] - 1);
+                ++slot_used[s];
+                tc::fence_after_sync();
+                return r;
+            };
+            while (ok && it.next(a, p)) {
+                // the row tiles
+                if (parts > 0) ok = wait(q_free, parts - 1);
+                if (!ok) break;
+                const int tiles = MODE == PAIR && p.rows > kTile ? 2 : 1;
+                tc::mbar_arrive_expect_tx(q_full, (uint32_t)(tiles * (D / 64) * C::SLICE));
+                for (int t = 0; t < tiles; ++t)
+                    for (int c = 0; c < D / 64; ++c)
+                        tc::tma_load_2d(sbase + (uint32_t)((t * (D / 64) + c) * C::SLICE), &qmap, 64 * c,
+                                        (int)p.row_id + t * kTile, q_full);
+                ok = tc::mbar_wait(q_full, (uint32_t)(parts & 1), fm::kWaitNs);
+                ++parts;
+                if constexpr (MODE == PAIR) {
+                    ok = ok && wait_tile(ring);
+                    if (!ok) break;
+                    for (int t = 0; t < tiles; ++t) qk(t, t, ring);
+                    release(ring++);
+                    if (p.tiles == 1) tc::commit(q_free);
+                    for (int j = 0; j < p.tiles && ok; ++j) {
+                        const int iv = ring, ik = ring + 1;
+                        ok = wait_tile(iv);
+                        for (int t = 0; t < tiles && ok; ++t) {
+                            ok = wait_weights(t, t, j == 0);
+                            if (!ok) break;
+                            pv(t, t, iv, j > 0);
+                            if (t == tiles - 1) release(iv);
+                            if (j + 1 < p.tiles) {
+                                if (t == 0) ok = wait_tile(ik);
+                                if (!ok) break;
+                                qk(t, t, ik);
+                                if (t == tiles - 1) release(ik);
+                            }
+                        }
+                        if (j + 2 == p.tiles) tc::commit(q_free);
+                        ring += j + 1 < p.tiles ? 2 : 1;
+                    }
+                    for (int t = 0; t < tiles; ++t) ++left[t];
+                } else {
+                    // key tile j is ahead of value tile j - 1
+                    auto scores = [&](int j) {
+                        const int s = MODE == STREAM ? j & 1 : (wide + j) & 1;
+                        if (!wait_tile(ring)) return false;
+                        qk(0, s, ring);
+                        release(ring);
+                        ring += NH;
+                        if (j + 1 == p.tiles) tc::commit(q_free);
+                        return true;
+                    };
+                    ok = ok && scores(0) && (p.tiles < 2 || scores(1));
+                    for (int j = 0; j < p.tiles && ok; ++j) {
+                        const int w = MODE == STREAM ? j & 1 : 0, s = MODE == STREAM ? w : (wide + j) & 1;
+                        const bool first = j < WGS;
+                        ok = wait_weights(w, s, first) && wait_tile(ring);
+                        if (!ok) break;
+                        pv(w, s, ring, !first);
+                        release(ring);
+                        ring += NH;
+                        if (j + 2 < p.tiles) ok = scores(j + 2);
+                    }
+                    wide += p.tiles;
+                    for (int w = 0; w < WGS; ++w)
+                        if (p.tiles > w) ++left[w];
+                }
+            }
+            if (!ok) {
+                // the MMAs in flight end before their columns are freed
+                *s_err = 1;
+                tc::commit(drained);
+                tc::mbar_wait(drained, 0u, fm::kWaitNs);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4 * WGS) {
+        // ---- unpacking: thread r has row r of every buffer ----
+        if constexpr (WGS == 2) regs_down<C::R_UNPACK>();
+        const int r = tid - 128 * WGS;
+        // items of a part, in the order that the MMAs take them: step j has the
+        // key tile j and the value tile j - LEAD
+        int step = 0, half = 0, what = 0;
+        bool more = it.next(a, p);
+        // Tile `tile` into L2, 16 rows by every 16th thread; the page was read
+        // a step earlier, so that nothing waits for it here.
+        int ahead = 0;
+        auto read_ahead = [&](int tile) {
+            const int t0 = tile * kTile + r;
+            ahead = t0 < p.rq.len ? __ldg(a.table + (int64_t)p.b * a.max_pages + (t0 >> a.page_shift)) : 0;
+        };
+        auto fetch_ahead = [&](int tile) {
+            const int t0 = tile * kTile + r;
+            if ((r & 15) != 0 || t0 >= p.rq.len) return;
+            const int pg = min(max(ahead, 0), a.n_pages - 1);
+            const int64_t row = (((int64_t)pg * a.n_kv_heads + p.hk) << a.page_shift) + (t0 & ((1 << a.page_shift) - 1));
+            auto pre = [](const void * ptr, uint32_t bytes) {
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(ptr), "r"(bytes) : "memory");
+            };
+            pre(a.k_codes + row * (D / 32 * a.k_bits), (uint32_t)(16 * D / 8 * a.k_bits));
+            pre(a.v_codes + row * (D / 32 * a.v_bits), (uint32_t)(16 * D / 8 * a.v_bits));
+            pre(a.k_norms + row * (D / 32), (uint32_t)(16 * D / 16));
+            pre(a.v_norms + row * (D / 32), (uint32_t)(16 * D / 16));
+        };
+        auto start_ahead = [&] {
+            for (int j = 1; j <= kTaAhead + 1; ++j) {
+                if (j < p.tiles) read_ahead(p.tile0 + j);
+                if (j < p.tiles && j <= kTaAhead) fetch_ahead(p.tile0 + j);
+            }
+        };
+        auto load = [&](Packed<NB> & x) {                    // the item at (step, what, half)
+            const int j = what == 0 ? step : step - LEAD;
+            const int t = (p.tile0 + j) * kTile + r;
+            const int bits = what == 0 ? a.k_bits : a.v_bits;
+            x.what = what;
+            x.half = half;
+#pragma unroll
+            for (int i = 0; i < NB / 2; ++i) x.norm[i] = x.other[i] = 0u;
+#pragma unroll
+            for (int i = 0; i < 4 * NB; ++i) x.w[i] = 0u;
+            if (t < p.rq.len) {
+                const int pg = min(max(a.table[(int64_t)p.b * a.max_pages + (t >> a.page_shift)], 0), a.n_pages - 1);
+                const int64_t row = (((int64_t)pg * a.n_kv_heads + p.hk) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
+                const uint32_t * c = (what == 0 ? a.k_codes : a.v_codes) + row * (D / 32 * bits) + half * (NB * bits);
+                if constexpr (NB == 4) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < bits) {
+                            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(c) + i);
+                            x.w[4 * i] = u.x; x.w[4 * i + 1] = u.y; x.w[4 * i + 2] = u.z; x.w[4 * i + 3] = u.w;
+                        }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < bits) {
+                            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(c) + i);
+                            x.w[2 * i] = u.x; x.w[2 * i + 1] = u.y;
+                        }
+                }
+                const uint32_t * kn = reinterpret_cast<const uint32_t *>(a.k_norms + row * (D / 32)) + half * (NB / 2);
+                const uint32_t * vn = reinterpret_cast<const uint32_t *>(a.v_norms + row * (D / 32)) + half * (NB / 2);
+#pragma unroll
+                for (int i = 0; i < NB / 2; ++i) {
+                    x.norm[i] = __ldg((what == 0 ? kn : vn) + i);
+                    if (what == 0) x.other[i] = __ldg(vn + i);
+                }
+            }
+        };
+        auto advance = [&] {
+            if (++half < NH) return;
+            half = 0;
+            // after the keys of this step its values, if any; then the next step
+            if (what == 0 && step >= LEAD) {
+                what = 1;
+                return;
+            }
+            what = 0;
+            if (++step < p.tiles) {
+                if (step + kTaAhead < p.tiles) fetch_ahead(p.tile0 + step + kTaAhead);
+                if (step + kTaAhead + 1 < p.tiles) read_ahead(p.tile0 + step + kTaAhead + 1);
+                return;
+            }
+            if (step < p.tiles + LEAD) {
+                what = 1;
+                return;
+            }
+            step = 0;
+            more = it.next(a, p);
+            if (more) start_ahead();
+        };
+        int ring = 0, tile = 0;
+        auto put = [&](Packed<NB> & x) {
+            const int s = ring % ST;
+            bool ok = ring < ST || (tc::mbar_wait(empty + 8u * s, (uint32_t)((ring / ST - 1) & 1), fm::kWaitNs) && *s_err == 0);
+            if (!__all_sync(0xffffffffu, ok)) {
+                *s_err = 1;
+                return false;
+            }
+            // a key with an infinite or NaN norm marks its readers' sums, and takes
+            // no part in the products
+            uint32_t bad = 0u;
+#pragma unroll
+            for (int i = 0; i < NB / 2; ++i)
+                bad |= ((x.norm[i] & 0x7C007C00u) + 0x04000400u) | ((x.other[i] & 0x7C007C00u) + 0x04000400u);
+            bad &= 0x80008000u;
+            if (x.what == 0) {
+                const uint32_t keys = __ballot_sync(0xffffffffu, bad != 0u);
+                if (lane == 0) {
+                    volatile uint32_t * word = s_bad + 4 * (tile & 7) + (warp - 4 * WGS);
+                    *word = x.half == 0 ? keys : *word | keys;
+                }
+                if (x.half == NH - 1) ++tile;
+            }
+            if (bad != 0u) {
+#pragma unroll
+                for (int i = 0; i < NB / 2; ++i) x.norm[i] = 0u;
+            }
+            unsigned char * dst = smem + C::OFF_RING + s * C::BUF + r * 128;
+            const int bits = x.what == 0 ? a.k_bits : a.v_bits;
+            uint32_t tab[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) tab[i] = x.what == 0 ? a.k_table[i] : a.v_table[i];
+            if (bits == 4) unpack_row<4, NB>(x.w, x.norm, tab, dst, r & 7);
+            else if (bits == 3) unpack_row<3, NB>(x.w, x.norm, tab, dst, r & 7);
+            else unpack_row<2, NB>(x.w, x.norm, tab, dst, r & 7);
+            tc::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(full + 8u * s);
+            ++ring;
+            return true;
+        };
+        Packed<NB> x, y;
+        bool in_x = more;
+        if (in_x) {
+            start_ahead();
+            load(x);
+            advance();
+        }
+        // one item is unpacked while the next one's words are on their way
+        while (in_x) {
+            const bool in_y = more;
+            if (in_y) {
+                load(y);
+                advance();
+            }
+            if (!put(x)) break;
+            if (!in_y) break;
+            in_x = more;
+            if (in_x) {
+                load(x);
+                advance();
+            }
+            if (!put(y)) break;
+        }
+    } else {
+        // ---- softmax: warpgroup w, one thread per row ----
+        regs_up<C::R_SOFTMAX>();
+        const int w = warp >> 2;
+        const int r = tid & 127;
+        const uint32_t lane_tm = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t o_tm = lane_tm + fm::kOutCol + (uint32_t)(w * D);
+        bool ok = true;
+        int tile0 = 0;                       // key tiles of the parts before
+        int mine = 0;                        // tiles that this warpgroup has done
+        while (ok && it.next(a, p)) {
+            const int in_set = MODE == PAIR ? w * kTile + r : r;       // row of the set
+            const bool valid = in_set < p.rows;
+            const bool takes = MODE == PAIR ? w * kTile < p.rows : MODE == STREAM ? w < p.tiles : true;
+            const int64_t id = p.row_id + in_set;
+            const bool own = p.tile0 == 0;
+            const int slot_row = w * kTile + r;
+            float2 * ml = own ? a.own_ml + (MODE == STREAM ? 2 * id + w : id)
+                              : a.more_ml + (int64_t)blockIdx.x * (2 * kTile) + slot_row;
+            if (!takes) {
+                if (MODE == STREAM && valid) *ml = make_float2(-CUDART_INF_F, 0.0f);
+                tile0 += p.tiles;
+                continue;
+            }
+            const int in_req = p.set * a.rows_per_set + in_set;
+            const int node = in_req / a.group;
+            const uint64_t * words = a.mask != nullptr && valid ? a.mask + (int64_t)(p.rq.r0 + node) * a.mask_words : nullptr;
+            const float mul = valid ? a.q_mul[id] : 0.0f;
+            const int ctx0 = p.rq.len - p.rq.n;                        // tokens before the nodes
+            const bool warp_valid = (MODE == PAIR ? w * kTile : 0) + (r & ~31) < p.rows;
+            fm::RowState st{-CUDART_INF_F, 0.0f};
+            bool first = true;
+            for (int j = MODE == STREAM ? w : 0; j < p.tiles; j += MODE == STREAM ? 2 : 1) {
+                const int slot = MODE == WIDE ? (tile0 + j) & 1 : w;
+                const int use = MODE == WIDE ? (tile0 + j) >> 1 : mine;
+                ok = tc::mbar_wait(s_full + 8u * slot, (uint32_t)(use & 1), fm::kWaitNs) && *s_err == 0;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc::fence_after_sync();
+                if (warp_valid) {
+                    const uint32_t s_tm = lane_tm + (uint32_t)slot * fm::kSlotCols;
+                    auto wait_acc = [&] { return tc::mbar_wait(o_done + 8u * w, (uint32_t)((mine - 1) & 1), fm::kWaitNs); };
+                    const int t0 = (p.tile0 + j) * kTile;
+                    uint32_t allowed[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+                    if (t0 + kTile > ctx0) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int c = p.rq.len - (t0 + 32 * x);    // tokens left
+                            const uint32_t in = c >= 32 ? 0xFFFFFFFFu : c <= 0 ? 0u : (1u << c) - 1u;
+                            allowed[x] = valid ? in & (in != 0u ? mask32(a, words, node, t0 + 32 * x - ctx0) : 0u) : 0u;
+                        }
+                        ok = fm::softmax_tile<false, true>(s_tm, o_tm, D, first, mul, allowed, st, wait_acc);
+                    } else {
+                        ok = fm::softmax_tile<false, false>(s_tm, o_tm, D, first, mul, nullptr, st, wait_acc);
+                    }
+                    const volatile uint32_t * bad = s_bad + 4 * ((tile0 + j) & 7);
+                    if (((bad[0] & allowed[0]) | (bad[1] & allowed[1]) | (bad[2] & allowed[2]) | (bad[3] & allowed[3])) != 0u)
+                        st.sum = CUDART_NAN_F;
+                }
+                first = false;
+                ++mine;
+                tc::mbar_arrive(p_full + 8u * slot);
+            }
+            tile0 += p.tiles;
+            // the last product (WIDE: the scores of a tile come before the products
+            // of the one in front of it, so that one is waited for first: a wait
+            // may be one phase ahead of the barrier, not two)
+            if (MODE == WIDE && mine > 1) ok = ok && tc::mbar_wait(o_done, (uint32_t)(mine & 1), fm::kWaitNs);
+            ok = ok && tc::mbar_wait(o_done + 8u * w, (uint32_t)((mine - 1) & 1), fm::kWaitNs);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (warp_valid) {
+                float * dst = own ? a.own + (MODE == STREAM ? 2 * id + w : id) * D
+                                  : a.more + ((int64_t)blockIdx.x * (2 * kTile) + slot_row) * D;
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    fm::tmem_ld32(o_tm + (uint32_t)c, o);
+                    if (valid) {
+#pragma unroll
+                        for (int x = 0; x < 32; x += 4)
+                            *reinterpret_cast<uint4 *>(dst + c + x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                    }
+                }
+                if (valid) *ml = make_float2(st.ref, st.sum);
+            }
+            tc::fence_before_sync();
+            tc::mbar_arrive(o_free + 8u * w);
+        }
+        if (!ok) *s_err = 1;
+    }
+    __syncthreads();
+    tc::fence_after_sync();
+    if (*s_err != 0 && tid == 0 && a.status != nullptr) atomicOr(a.status, TQ_STATUS_TIMEOUT);
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// Merge and rotation back: one warp per (row, head)
+// ---------------------------------------------------------------------------
+
+constexpr int kTmThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kTmThreads) tree_combine_kernel(const __grid_constant__ TreeArgs a) {
+    constexpr int E = D / 32, NW = kTmThreads / 32;
+    __shared__ float y_s[NW][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t vec = (int64_t)blockIdx.x * NW + warp;
+    if (vec >= (int64_t)a.n_rows * a.n_q_heads) return;
+    const int row = (int)(vec / a.n_q_heads), h = (int)(vec - (int64_t)row * a.n_q_heads);
+    const int b = request_of_row(a, row);
+    const Request q = request_of(a, b);
+    const int node = row - q.r0;
+    if (node < 0 || node >= q.n) return;
+    const int hk = h / a.group, in_req = node * a.group + h - hk * a.group;
+    const int set = in_req / a.rows_per_set, in_set = in_req - set * a.rows_per_set;
+    const int64_t id = (int64_t)q.r0 * a.n_q_heads + (int64_t)hk * q.n * a.group + in_req;
+    const int64_t units = a.unit0[a.batch];
+    const int tiles = tiles_of(q.len);
+    const int64_t u0 = a.unit0[b] + ((int64_t)hk * sets_of(a, q.n) + set) * tiles;
+    float ref = -CUDART_INF_F, sum = 0.0f, v[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) v[k] = 0.0f;
+    auto add = [&](float2 ml, const float * o) {
+        if (ml.x == -CUDART_INF_F) return;               // no key attended
+        const float top = fmaxf(ref, ml.x);              // (a NaN stays in the sums)
+        const float fa = ref == -CUDART_INF_F ? 0.0f : fm::ex2(ref - top), fb = fm::ex2(ml.x - top);
+        ref = top;
+        sum = sum * fa + ml.y * fb;
+#pragma unroll
+        for (int k = 0; k < E; k += 2) {
+            const float2 x = *reinterpret_cast<const float2 *>(o + E * lane + k);
+            v[k] = v[k] * fa + x.x * fb;
+            v[k + 1] = v[k + 1] * fa + x.y * fb;
+        }
+    };
+    if (tiles > 0) {
+        const int64_t n = sharers(a, units);
+        const int c0 = cta_of(u0, units, n), c1 = cta_of(u0 + tiles - 1, units, n);
+        for (int s = 0; s < a.streams; ++s) add(a.own_ml[id * a.streams + s], a.own + (id * a.streams + s) * D);
+        for (int c = c0 + 1; c <= c1; ++c)
+            for (int s = 0; s < a.streams; ++s) {
+                const int64_t at = (int64_t)c * (2 * kTile) + s * kTile + in_set;
+                add(a.more_ml[at], a.more + at * D);
+            }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a node that attends nothing: zeros
+#pragma unroll
+    for (int k = 0; k < E; ++k) v[k] *= inv;
+    if (a.dense) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) y_s[warp][E * lane + k] = v[k];
+        __syncwarp();
+        float x[E];
+#pragma unroll
+        for (int k = 0; k < E; ++k) x[k] = 0.0f;
+        for (int e = 0; e < D; ++e) {
+            const float y = y_s[warp][e];
+#pragma unroll
+            for (int k = 0; k < E; ++k) x[k] = fmaf(__ldg(a.rot_f32 + (int64_t)e * D + 32 * k + lane), y, x[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < E; ++k) store_el(a.out, a.q_dtype, vec * D + 32 * k + lane, x[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < E; ++k) v[k] = signed_by(a.d1_bits, E * lane + k, v[k]);
+        warp_fwht<E>(v, lane);
+#pragma unroll
+        for (int k = 0; k < E; ++k) store_el(a.out, a.q_dtype, vec * D + E * lane + k, signed_by(a.d2_bits, E * lane + k, v[k]));
+    }
+}
+
+template <int D, int MODE>
+int launch_tree_main(const TreeArgs & a, cudaStream_t st) {
+    using C = TaCfg<D, MODE>;
+    CUtensorMap qmap;
+    if (!encode_tensor_map_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.q_rows, (uint64_t)D,
+                              (uint64_t)a.n_rows * a.n_q_heads, (uint64_t)D * 2, 64u, (uint32_t)kTile,
+                              CU_TENSOR_MAP_SWIZZLE_128B))
+        return (int)cudaErrorInvalidValue;
+    auto k = tree_kernel<D, MODE>;
+    if (int e = ensure_dynamic_smem(reinterpret_cast<const void *>(k), C::SMEM)) return e;
+    k<<<(unsigned)a.n_ctas, C::THREADS, C::SMEM, st>>>(a, qmap);
     return (int)cudaGetLastError();
 }
 
 template <int D>
-int launch_tree(const TreeArgs & a, int kb, int vb, cudaStream_t st) {
-    return kb == 2 ? launch_tree_v<D, 2>(a, vb, st) : kb == 3 ? launch_tree_v<D, 3>(a, vb, st)
-                                                             : launch_tree_v<D, 4>(a, vb, st);
+int launch_tree(TreeArgs & a, cudaStream_t st) {
+    const unsigned vecs = (unsigned)(((int64_t)a.n_rows * a.n_q_heads + 7) / 8);
+    tree_prep_kernel<D><<<vecs + 1, kTpThreads, 0, st>>>(a);
+    if (int e = (int)cudaGetLastError()) return e;
+    int e;
+    if constexpr (D == 256) e = launch_tree_main<D, WIDE>(a, st);
+    else e = a.streams == 2 ? launch_tree_main<D, STREAM>(a, st) : launch_tree_main<D, PAIR>(a, st);
+    if (e) return e;
+    tree_combine_kernel<D><<<vecs, kTmThreads, 0, st>>>(a);
+    return (int)cudaGetLastError();
+}
+
+// Workspace sections, each from a 256-byte boundary.
+struct TreeSpace {
+    size_t unit0, q_rows, q_mul, own, own_ml, more, more_ml, total;
+};
+TreeSpace tree_space(int64_t batch, int64_t vecs, int d, int n_ctas) {
+    TreeSpace s;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    s.unit0 = take((size_t)(batch + 1) * 8);
+    s.q_rows = take((size_t)vecs * d * 2);
+    s.q_mul = take((size_t)vecs * 4);
+    s.own = take((size_t)vecs * 2 * d * 4);
+    s.own_ml = take((size_t)vecs * 2 * 8);
+    s.more = take((size_t)n_ctas * 2 * kTile * d * 4);
+    s.more_ml = take((size_t)n_ctas * 2 * kTile * 8);
+    s.total = at;
+    return s;
+}
+
+// fp16 bits of the centroids as byte tables (entries above 2^bits - 1 repeat the last)
+void centroid_table(const CodebookParams & cb, int bits, uint32_t * tab) {
+    for (int i = 0; i < 8; ++i) tab[i] = 0u;
+    for (int i = 0; i < 16; ++i) {
+        const __half_raw h = __float2half_rn(cb.centroid[i < (1 << bits) ? i : (1 << bits) - 1]);
+        tab[i >> 2] |= (uint32_t)(h.x & 0xFFu) << (8 * (i & 3));
+        tab[4 + (i >> 2)] |= (uint32_t)(h.x >> 8) << (8 * (i & 3));
+    }
 }
 
 bool tree_sizes_ok(int32_t batch, int32_t n_rows, int32_t max_nodes, int32_t n_q_heads, int32_t n_kv_heads,
@@ -194,7 +1010,7 @@ extern "C" size_t tq_tree_workspace_size(int32_t batch, int32_t n_rows, int32_t 
                                          int32_t n_kv_heads, int64_t max_len, int32_t head_dim) {
     const char * why;
     if (!tree_sizes_ok(batch, n_rows, max_nodes, n_q_heads, n_kv_heads, max_len, head_dim, &why)) return 0;
-    return 256;
+    return tree_space(batch, (int64_t)n_rows * n_q_heads, head_dim, device_sm_count()).total;
 }
 
 extern "C" tq_status tq_tree_attention(const tq_rotation * rot, int32_t k_bits, int32_t v_bits, int32_t block,
@@ -269,14 +1085,26 @@ extern "C" tq_status tq_tree_attention(const tq_rotation * rot, int32_t k_bits, 
         a.d1_bits[i] = rot->d1_bits[i];
         a.d2_bits[i] = rot->d2_bits[i];
     }
-    for (int i = 0; i < kMaxLevels; ++i) {
-        a.kc[i] = kcb.centroid[i];
-        a.vc[i] = vcb.centroid[i];
-    }
+    a.k_bits = k_bits;
+    a.v_bits = v_bits;
+    centroid_table(kcb, k_bits, a.k_table);
+    centroid_table(vcb, v_bits, a.v_table);
+    a.group = n_q_heads / n_kv_heads;
+    a.n_ctas = device_sm_count();
+    a.streams = head_dim < 256 && (int64_t)max_nodes * a.group <= kTile ? 2 : 1;
+    a.rows_per_set = head_dim < 256 && a.streams == 1 ? 2 * kTile : kTile;
+    unsigned char * ws = static_cast<unsigned char *>(workspace);
+    const TreeSpace sp = tree_space(batch, (int64_t)n_rows * n_q_heads, head_dim, a.n_ctas);
+    a.unit0 = reinterpret_cast<int64_t *>(ws + sp.unit0);
+    a.q_rows = reinterpret_cast<__half *>(ws + sp.q_rows);
+    a.q_mul = reinterpret_cast<float *>(ws + sp.q_mul);
+    a.own = reinterpret_cast<float *>(ws + sp.own);
+    a.own_ml = reinterpret_cast<float2 *>(ws + sp.own_ml);
+    a.more = reinterpret_cast<float *>(ws + sp.more);
+    a.more_ml = reinterpret_cast<float2 *>(ws + sp.more_ml);
     a.out = out;
     a.status = status_dev;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int e = head_dim == 64 ? launch_tree<64>(a, k_bits, v_bits, s)
-                : head_dim == 128 ? launch_tree<128>(a, k_bits, v_bits, s) : launch_tree<256>(a, k_bits, v_bits, s);
+    const int e = head_dim == 64 ? launch_tree<64>(a, s) : head_dim == 128 ? launch_tree<128>(a, s) : launch_tree<256>(a, s);
     return cuda_status(e, "tree attention launch");
 }
