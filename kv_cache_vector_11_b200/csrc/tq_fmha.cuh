@@ -24,6 +24,18 @@ constexpr uint32_t kSlotCols = 128;            // TMEM columns of a score slot
 constexpr uint32_t kOutCol = 256;              // first column of the output accumulators
 constexpr uint64_t kWaitNs = 1000000000ull;    // bound of every wait
 
+// 16 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t * r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15"
+        "}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr) : "memory");
+}
+
 // 32 consecutive 32-bit columns of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t * r) {
     asm volatile(
@@ -77,6 +89,17 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t * r) {
           "=&r"(r[112]), "=&r"(r[113]), "=&r"(r[114]), "=&r"(r[115]), "=&r"(r[116]), "=&r"(r[117]), "=&r"(r[118]), "=&r"(r[119]),
           "=&r"(r[120]), "=&r"(r[121]), "=&r"(r[122]), "=&r"(r[123]), "=&r"(r[124]), "=&r"(r[125]), "=&r"(r[126]), "=&r"(r[127])
         : "r"(taddr), "r"(taddr + 32u), "r"(taddr + 64u), "r"(taddr + 96u) : "memory");
+}
+
+// 16 32-bit values into consecutive columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t * r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+        "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16"
+        "};"
+        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
 }
 
 // 32 32-bit values into consecutive columns of this thread's TMEM lane.
@@ -197,12 +220,12 @@ __device__ __forceinline__ bool softmax_tile(uint32_t s_tm, uint32_t o_tm, int o
         st.sum *= f;
         ok = wait_acc();
         tc::fence_after_sync();
-        for (int c = 0; c < o_cols; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_tm + (uint32_t)c, o);
+        for (int c = 0; c < o_cols; c += 16) {           // (few registers: the scores are live)
+            uint32_t o[16];
+            tmem_ld16(o_tm + (uint32_t)c, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st32(o_tm + (uint32_t)c, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(o_tm + (uint32_t)c, o);
         }
     }
     const float bias = kShift<BF16> - (st.ref == -CUDART_INF_F ? 0.0f : st.ref);

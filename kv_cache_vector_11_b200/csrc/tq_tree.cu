@@ -389,19 +389,24 @@ struct TaCfg {
     static constexpr int QT = MODE == PAIR ? 2 : 1;      // row tiles
     static constexpr int LEAD = MODE == PAIR ? 0 : 1;    // tiles that the keys are ahead of the values
     static constexpr int OFF_RING = QT * NH * BUF;
-    static constexpr int STAGES = (224 * 1024 - OFF_RING) / BUF < 8 ? (224 * 1024 - OFF_RING) / BUF : 8;
+    static constexpr int STAGES = (192 * 1024 - OFF_RING) / BUF < 8 ? (192 * 1024 - OFF_RING) / BUF : 8;
     static constexpr int THREADS = 128 * (WGS + 2);      // softmax, unpacking, MMAs
+    // packed rows on their way: codes as 4 chunks x 128 threads x CHUNK bytes,
+    // then the norms and the other norms, 2 NB bytes a thread
+    static constexpr int CHUNK = 4 * NB, NORMS = 2 * NB;
+    static constexpr int OFF_PACKED = OFF_RING + STAGES * BUF;
+    static constexpr int PACKED = kTile * (4 * CHUNK + 2 * NORMS);
     // mbarriers: full[STAGES], empty[STAGES], s_full[2], p_full[2], o_done[2],
     // o_free[2], q_full, q_free, drained
-    static constexpr int OFF_BAR = OFF_RING + STAGES * BUF;
+    static constexpr int OFF_BAR = OFF_PACKED + 3 * PACKED;
     static constexpr int N_BAR = 2 * STAGES + 11;
     static constexpr int OFF_BAD = (OFF_BAR + 8 * N_BAR + 15) / 16 * 16;    // 8 tiles x 128 bits: keys with a bad norm
     static constexpr int OFF_MISC = OFF_BAD + 128;                           // TMEM address, error flag, first request
     static constexpr int SMEM = OFF_MISC + 16 + 1024;                       // + alignment of the base
     static_assert(SMEM <= 232448, "shared memory of a CTA");
     // registers a thread: the launch's share is 128 (512 threads) or 168 (384)
-    static constexpr int R_SOFTMAX = WGS == 2 ? 184 : 240;
-    static constexpr int R_UNPACK = WGS == 2 ? 96 : 168;
+    static constexpr int R_SOFTMAX = WGS == 2 ? 192 : 240;
+    static constexpr int R_UNPACK = WGS == 2 ? 80 : 168;
     static constexpr int R_MMA = WGS == 2 ? 48 : 96;
     static_assert(WGS * R_SOFTMAX + R_UNPACK + R_MMA <= (WGS == 2 ? 512 : 504), "no more than the launch holds");
 };
@@ -411,15 +416,11 @@ __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.al
 template <int N>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
 
-// A row's packed words of one buffer, in flight.
-template <int NB>
-struct Packed {
-    uint32_t w[4 * NB];
-    uint32_t norm[NB / 2];                           // of its blocks, two to a word
-    uint32_t other[NB / 2];                          // keys: the values' norms (read for the check alone)
-    int what;                                        // 0: keys, 1: values
-    int half;
-};
+// Asynchronous copy of N bytes into shared memory, zeros where !live.
+template <int N>
+__device__ __forceinline__ void copy_or_zero(uint32_t dst, const void * src, bool live) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" :: "r"(dst), "l"(src), "n"(N), "r"(live ? N : 0) : "memory");
+}
 
 template <int D, int MODE>
 __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const __grid_constant__ TreeArgs a,
@@ -631,43 +632,28 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                 if (j < p.tiles && j <= kTaAhead) fetch_ahead(p.tile0 + j);
             }
         };
-        auto load = [&](Packed<NB> & x) {                    // the item at (step, what, half)
+        // The packed words and norms of this thread's row of the item at (step,
+        // what, half), into slot `slot`; every thread reads back only what it
+        // copied itself.
+        const uint32_t packed = sbase + (uint32_t)C::OFF_PACKED;
+        auto fetch = [&](int slot) {
             const int j = what == 0 ? step : step - LEAD;
             const int t = (p.tile0 + j) * kTile + r;
+            const bool live = t < p.rq.len;
             const int bits = what == 0 ? a.k_bits : a.v_bits;
-            x.what = what;
-            x.half = half;
+            int pg = 0;
+            if (live) pg = min(max(__ldg(a.table + (int64_t)p.b * a.max_pages + (t >> a.page_shift)), 0), a.n_pages - 1);
+            const int64_t row = live ? (((int64_t)pg * a.n_kv_heads + p.hk) << a.page_shift) + (t & ((1 << a.page_shift) - 1)) : 0;
+            const uint32_t * c = (what == 0 ? a.k_codes : a.v_codes) + row * (D / 32 * bits) + half * (NB * bits);
+            const uint32_t dst = packed + (uint32_t)(slot * C::PACKED);
 #pragma unroll
-            for (int i = 0; i < NB / 2; ++i) x.norm[i] = x.other[i] = 0u;
-#pragma unroll
-            for (int i = 0; i < 4 * NB; ++i) x.w[i] = 0u;
-            if (t < p.rq.len) {
-                const int pg = min(max(a.table[(int64_t)p.b * a.max_pages + (t >> a.page_shift)], 0), a.n_pages - 1);
-                const int64_t row = (((int64_t)pg * a.n_kv_heads + p.hk) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
-                const uint32_t * c = (what == 0 ? a.k_codes : a.v_codes) + row * (D / 32 * bits) + half * (NB * bits);
-                if constexpr (NB == 4) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i < bits) {
-                            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(c) + i);
-                            x.w[4 * i] = u.x; x.w[4 * i + 1] = u.y; x.w[4 * i + 2] = u.z; x.w[4 * i + 3] = u.w;
-                        }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i < bits) {
-                            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(c) + i);
-                            x.w[2 * i] = u.x; x.w[2 * i + 1] = u.y;
-                        }
-                }
-                const uint32_t * kn = reinterpret_cast<const uint32_t *>(a.k_norms + row * (D / 32)) + half * (NB / 2);
-                const uint32_t * vn = reinterpret_cast<const uint32_t *>(a.v_norms + row * (D / 32)) + half * (NB / 2);
-#pragma unroll
-                for (int i = 0; i < NB / 2; ++i) {
-                    x.norm[i] = __ldg((what == 0 ? kn : vn) + i);
-                    if (what == 0) x.other[i] = __ldg(vn + i);
-                }
-            }
+            for (int i = 0; i < 4; ++i)
+                if (i < bits) copy_or_zero<C::CHUNK>(dst + (uint32_t)((i * kTile + r) * C::CHUNK), c + i * NB, live);
+            const uint16_t * kn = a.k_norms + row * (D / 32) + half * NB;
+            const uint16_t * vn = a.v_norms + row * (D / 32) + half * NB;
+            const uint32_t nd = dst + (uint32_t)(kTile * 4 * C::CHUNK + r * C::NORMS);
+            copy_or_zero<C::NORMS>(nd, what == 0 ? kn : vn, live);
+            if (what == 0) copy_or_zero<C::NORMS>(nd + (uint32_t)(kTile * C::NORMS), vn, live);
         };
         auto advance = [&] {
             if (++half < NH) return;
@@ -691,70 +677,92 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
             more = it.next(a, p);
             if (more) start_ahead();
         };
-        int ring = 0, tile = 0;
-        auto put = [&](Packed<NB> & x) {
+        // Three items are on their way while one is unpacked; flags: bit 0 values,
+        // bit 1 second half.
+        int ring = 0, tile = 0, slot = 0, flags[3], left = 0;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            flags[k] = 0;
+            if (more) {
+                if (k == 0) start_ahead();
+                fetch(k);
+                flags[k] = what | half << 1;
+                ++left;
+                advance();
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        while (left > 0) {
             const int s = ring % ST;
-            bool ok = ring < ST || (tc::mbar_wait(empty + 8u * s, (uint32_t)((ring / ST - 1) & 1), fm::kWaitNs) && *s_err == 0);
+            const bool ok = ring < ST || (tc::mbar_wait(empty + 8u * s, (uint32_t)((ring / ST - 1) & 1), fm::kWaitNs) && *s_err == 0);
             if (!__all_sync(0xffffffffu, ok)) {
                 *s_err = 1;
-                return false;
+                break;
             }
+            asm volatile("cp.async.wait_group 2;" ::: "memory");
+            const unsigned char * src = smem + C::OFF_PACKED + slot * C::PACKED;
+            uint32_t w[4 * NB], norm[NB / 2], other[NB / 2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (NB == 4) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(src + (i * kTile + r) * 16);
+                    w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(src + (i * kTile + r) * 8);
+                    w[2 * i] = u.x; w[2 * i + 1] = u.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NB / 2; ++i) {
+                const uint32_t * n = reinterpret_cast<const uint32_t *>(src + kTile * 4 * C::CHUNK + r * C::NORMS) + i;
+                norm[i] = n[0];
+                other[i] = n[kTile * NB / 2];
+            }
+            const int item = flags[0];
+            flags[0] = flags[1];
+            flags[1] = flags[2];
+            --left;
             // a key with an infinite or NaN norm marks its readers' sums, and takes
             // no part in the products
             uint32_t bad = 0u;
 #pragma unroll
             for (int i = 0; i < NB / 2; ++i)
-                bad |= ((x.norm[i] & 0x7C007C00u) + 0x04000400u) | ((x.other[i] & 0x7C007C00u) + 0x04000400u);
+                bad |= ((norm[i] & 0x7C007C00u) + 0x04000400u) | (item & 1 ? 0u : (other[i] & 0x7C007C00u) + 0x04000400u);
             bad &= 0x80008000u;
-            if (x.what == 0) {
+            if ((item & 1) == 0) {
                 const uint32_t keys = __ballot_sync(0xffffffffu, bad != 0u);
                 if (lane == 0) {
                     volatile uint32_t * word = s_bad + 4 * (tile & 7) + (warp - 4 * WGS);
-                    *word = x.half == 0 ? keys : *word | keys;
+                    *word = item == 0 ? keys : *word | keys;
                 }
-                if (x.half == NH - 1) ++tile;
+                if (NH == 1 || item != 0) ++tile;
             }
             if (bad != 0u) {
 #pragma unroll
-                for (int i = 0; i < NB / 2; ++i) x.norm[i] = 0u;
+                for (int i = 0; i < NB / 2; ++i) norm[i] = 0u;
             }
+            if (more) {
+                fetch(slot);
+                flags[2] = what | half << 1;
+                ++left;
+                advance();
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            slot = slot == 2 ? 0 : slot + 1;
             unsigned char * dst = smem + C::OFF_RING + s * C::BUF + r * 128;
-            const int bits = x.what == 0 ? a.k_bits : a.v_bits;
+            const int bits = item & 1 ? a.v_bits : a.k_bits;
             uint32_t tab[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) tab[i] = x.what == 0 ? a.k_table[i] : a.v_table[i];
-            if (bits == 4) unpack_row<4, NB>(x.w, x.norm, tab, dst, r & 7);
-            else if (bits == 3) unpack_row<3, NB>(x.w, x.norm, tab, dst, r & 7);
-            else unpack_row<2, NB>(x.w, x.norm, tab, dst, r & 7);
+            for (int i = 0; i < 8; ++i) tab[i] = item & 1 ? a.v_table[i] : a.k_table[i];
+            if (bits == 4) unpack_row<4, NB>(w, norm, tab, dst, r & 7);
+            else if (bits == 3) unpack_row<3, NB>(w, norm, tab, dst, r & 7);
+            else unpack_row<2, NB>(w, norm, tab, dst, r & 7);
             tc::fence_proxy_async();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(full + 8u * s);
             ++ring;
-            return true;
-        };
-        Packed<NB> x, y;
-        bool in_x = more;
-        if (in_x) {
-            start_ahead();
-            load(x);
-            advance();
         }
-        // one item is unpacked while the next one's words are on their way
-        while (in_x) {
-            const bool in_y = more;
-            if (in_y) {
-                load(y);
-                advance();
-            }
-            if (!put(x)) break;
-            if (!in_y) break;
-            in_x = more;
-            if (in_x) {
-                load(x);
-                advance();
-            }
-            if (!put(y)) break;
-        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else {
         // ---- softmax: warpgroup w, one thread per row ----
         regs_up<C::R_SOFTMAX>();
