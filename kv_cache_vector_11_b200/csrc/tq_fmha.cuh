@@ -3,9 +3,15 @@
 // the output accumulators in TMEM, one softmax thread per row.
 //
 // TMEM (512 columns, 128 lanes = the tile's rows): two score slots of 128 fp32
-// columns at 0 and 128, the output accumulators from column 256 on.  A row's
-// weights are written back as 16-bit pairs over the first 64 columns of its
-// score slot, which the second product reads as its A operand.
+// columns at 0 and 128, the output accumulators from column 256 on.  A slot is
+// two halves of 64 keys with barriers of their own, so that the products and the
+// next scores of one half are under way during the softmax of the other.  A
+// row's weights are written back as 16-bit pairs over the first 32 columns of
+// their half, which the second product reads as its A operand.
+//
+// A wait on an mbarrier names a phase by its parity, so the barrier may be at
+// that phase or one past it when the wait begins, not further: every wait below
+// says why it is not.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -21,6 +27,7 @@ namespace fm {
 
 constexpr int kTile = 128;                     // rows of a query tile, keys of a key tile
 constexpr uint32_t kSlotCols = 128;            // TMEM columns of a score slot
+constexpr uint32_t kHalfCols = 64;             // of them, the scores of half a key tile
 constexpr uint32_t kOutCol = 256;              // first column of the output accumulators
 constexpr uint64_t kWaitNs = 1000000000ull;    // bound of every wait
 
@@ -51,44 +58,29 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t * r) {
         : "r"(taddr) : "memory");
 }
 
-// 128 consecutive 32-bit columns of this thread's TMEM lane.  One statement, so
-// that no use of a register can move in front of the wait.
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t * r) {
+// The same without the wait: r holds the columns after tmem_wait32(r).
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t * r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
         "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,"
         "%27,%28,%29,%30,%31"
-        "}, [%128];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,"
-        "%57,%58,%59,%60,%61,%62,%63"
-        "}, [%129];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-        "%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,"
-        "%89,%90,%91,%92,%93,%94,%95"
-        "}, [%130];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-        "%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,"
-        "%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127"
-        "}, [%131];\n\t"
+        "}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr) : "memory");
+}
+// Waits for all loads of this thread; r is an operand, so that no use of it can
+// move in front of the wait.
+__device__ __forceinline__ void tmem_wait32(uint32_t * r) {
+    asm volatile(
         "tcgen05.wait::ld.sync.aligned;"
-        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]),
-          "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]),
-          "=&r"(r[16]), "=&r"(r[17]), "=&r"(r[18]), "=&r"(r[19]), "=&r"(r[20]), "=&r"(r[21]), "=&r"(r[22]), "=&r"(r[23]),
-          "=&r"(r[24]), "=&r"(r[25]), "=&r"(r[26]), "=&r"(r[27]), "=&r"(r[28]), "=&r"(r[29]), "=&r"(r[30]), "=&r"(r[31]),
-          "=&r"(r[32]), "=&r"(r[33]), "=&r"(r[34]), "=&r"(r[35]), "=&r"(r[36]), "=&r"(r[37]), "=&r"(r[38]), "=&r"(r[39]),
-          "=&r"(r[40]), "=&r"(r[41]), "=&r"(r[42]), "=&r"(r[43]), "=&r"(r[44]), "=&r"(r[45]), "=&r"(r[46]), "=&r"(r[47]),
-          "=&r"(r[48]), "=&r"(r[49]), "=&r"(r[50]), "=&r"(r[51]), "=&r"(r[52]), "=&r"(r[53]), "=&r"(r[54]), "=&r"(r[55]),
-          "=&r"(r[56]), "=&r"(r[57]), "=&r"(r[58]), "=&r"(r[59]), "=&r"(r[60]), "=&r"(r[61]), "=&r"(r[62]), "=&r"(r[63]),
-          "=&r"(r[64]), "=&r"(r[65]), "=&r"(r[66]), "=&r"(r[67]), "=&r"(r[68]), "=&r"(r[69]), "=&r"(r[70]), "=&r"(r[71]),
-          "=&r"(r[72]), "=&r"(r[73]), "=&r"(r[74]), "=&r"(r[75]), "=&r"(r[76]), "=&r"(r[77]), "=&r"(r[78]), "=&r"(r[79]),
-          "=&r"(r[80]), "=&r"(r[81]), "=&r"(r[82]), "=&r"(r[83]), "=&r"(r[84]), "=&r"(r[85]), "=&r"(r[86]), "=&r"(r[87]),
-          "=&r"(r[88]), "=&r"(r[89]), "=&r"(r[90]), "=&r"(r[91]), "=&r"(r[92]), "=&r"(r[93]), "=&r"(r[94]), "=&r"(r[95]),
-          "=&r"(r[96]), "=&r"(r[97]), "=&r"(r[98]), "=&r"(r[99]), "=&r"(r[100]), "=&r"(r[101]), "=&r"(r[102]), "=&r"(r[103]),
-          "=&r"(r[104]), "=&r"(r[105]), "=&r"(r[106]), "=&r"(r[107]), "=&r"(r[108]), "=&r"(r[109]), "=&r"(r[110]), "=&r"(r[111]),
-          "=&r"(r[112]), "=&r"(r[113]), "=&r"(r[114]), "=&r"(r[115]), "=&r"(r[116]), "=&r"(r[117]), "=&r"(r[118]), "=&r"(r[119]),
-          "=&r"(r[120]), "=&r"(r[121]), "=&r"(r[122]), "=&r"(r[123]), "=&r"(r[124]), "=&r"(r[125]), "=&r"(r[126]), "=&r"(r[127])
-        : "r"(taddr), "r"(taddr + 32u), "r"(taddr + 64u), "r"(taddr + 96u) : "memory");
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+          "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+          "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+          "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+        :: "memory");
 }
 
 // 16 32-bit values into consecutive columns of this thread's TMEM lane.
@@ -102,19 +94,31 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t * r) {
         : "memory");
 }
 
-// 32 32-bit values into consecutive columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t * r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
-        "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
-        "%28,%29,%30,%31,%32"
-        "};"
-        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-           "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-           "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
+// Bounded wait for a phase of an mbarrier.  The waiting thread sleeps: polling
+// instead answers some 150 cycles earlier, but takes issue slots from the
+// softmax (8192-token prompt 0.556 ms against 0.504 ms).
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+    if (tc::mbar_try(bar, parity)) return true;
+    const uint64_t t0 = tc::global_ns();
+#pragma unroll 1
+    for (uint32_t i = 0; i < (1u << 30); ++i) {
+        if (tc::mbar_try_sleep(bar, parity, 20000u)) return true;
+        if (tc::global_ns() - t0 > kWaitNs) return false;
+    }
+    return false;
 }
+
+// Position in a ring of N buffers: the buffer and the parity of its use.
+template <int N>
+struct Ring {
+    uint32_t at = 0, parity = 0;
+    __device__ __forceinline__ void step() {
+        if (++at == N) {
+            at = 0;
+            parity ^= 1u;
+        }
+    }
+};
 
 __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -129,6 +133,13 @@ __device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
         :: "r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+// The same value; keeps the compiler from holding sums of it in registers
+// across a loop.
+__device__ __forceinline__ uint64_t opaque(uint64_t x) {
+    asm volatile("" : "+l"(x));
+    return x;
 }
 
 // Descriptor of a value tile as the second product's B operand: rows of 64
@@ -158,6 +169,31 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Two fp32 values in one 64-bit register pair, multiplied or added at once.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// The largest of three (a NaN is passed over).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     if constexpr (BF16) {
@@ -184,66 +220,90 @@ struct RowState {
     float sum;
 };
 
-// One tile of scores: reads slot `s_tm` (lane included), drops the columns
-// whose bit in `allowed` is clear (MASKED), updates the row's state, rescales
-// the accumulator at `o_tm` (o_cols columns) where needed -- after
-// wait_acc() says that the products of the tiles before are done -- and writes
-// the weights.  All 32 lanes of the warp call it together.
-template <bool BF16, bool MASKED, typename WaitAcc>
-__device__ __forceinline__ bool softmax_tile(uint32_t s_tm, uint32_t o_tm, int o_cols, bool first, float mul,
-                                             const uint32_t * allowed, RowState & st, WaitAcc wait_acc) {
-    uint32_t r[128];
-    tmem_ld128(s_tm, r);
+// Maximum of 32 scores.
+__device__ __forceinline__ float top32(const uint32_t * r) {
+    float m[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) m[i] = max3(__uint_as_float(r[i]), __uint_as_float(r[i + 2]), __uint_as_float(r[i + 4]));
+#pragma unroll
+    for (int c = 6; c < 30; c += 4)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) m[i] = max3(m[i], __uint_as_float(r[c + i]), __uint_as_float(r[c + 2 + i]));
+    return fmaxf(max3(m[0], m[1], __uint_as_float(r[30])), __uint_as_float(r[31]));
+}
+
+// Weights of 32 scores into the 16 columns at p_tm, and onto the sum.  (All
+// exponentials on the special-function unit: a polynomial on the FMA units for
+// one pair in eight, four or three cost 4, 6 and 8 % of the 8192-token prompt's
+// time, for the instructions, although that unit is half busy.)
+template <bool BF16>
+__device__ __forceinline__ void weights32(const uint32_t * r, uint64_t mul, uint64_t bias, uint32_t p_tm, uint64_t * sum) {
+    uint32_t w[16];
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+        const uint64_t x = fma2(pair(r[c], r[c + 1]), mul, bias);
+        const float a = ex2(__uint_as_float((uint32_t)x)), b = ex2(__uint_as_float((uint32_t)(x >> 32)));
+        sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pair(a, b));
+        w[c >> 1] = pack2<BF16>(a, b);
+    }
+    tmem_st16(p_tm, w);
+}
+
+template <bool MASKED>
+__device__ __forceinline__ void drop32(uint32_t * r, uint32_t allowed) {
     if constexpr (MASKED) {
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-            if (!((allowed[c >> 5] >> (c & 31)) & 1u)) r[c] = 0xFF800000u;
+        for (int c = 0; c < 32; ++c)
+            if (!((allowed >> c) & 1u)) r[c] = 0xFF800000u;
     }
-    float mx[4];
+}
+
+// Multiplies cols columns of this thread's accumulator by f.
+__device__ __forceinline__ void rescale(uint32_t o_tm, int cols, float f) {
+    tc::fence_after_sync();
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 16) {
+        uint32_t o[16];
+        tmem_ld16(o_tm + (uint32_t)c, o);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(r[i]);
-#pragma unroll
-    for (int c = 4; c < 128; c += 8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            mx[i] = c + 4 + i < 128 ? fmaxf(fmaxf(mx[i], __uint_as_float(r[c + i])), __uint_as_float(r[c + 4 + i]))
-                                    : fmaxf(mx[i], __uint_as_float(r[c + i]));
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tmem_st16(o_tm + (uint32_t)c, o);
     }
-    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+}
+
+// Half a tile of scores (64 keys): reads the 64 columns at `s_tm` (lane
+// included), drops those whose bit in `allowed` is clear (MASKED), updates the
+// row's state, has the accumulator multiplied where needed -- scale_acc(f) waits
+// for the products so far and multiplies the row by f -- and writes the weights over the first 32 of the columns.  All 32 lanes of the warp call it
+// together.
+template <bool BF16, bool MASKED, typename ScaleAcc>
+__device__ __forceinline__ bool softmax_half(uint32_t s_tm, bool first, float mul, const uint32_t * allowed, RowState & st,
+                                             ScaleAcc scale_acc) {
+    uint32_t r0[32], r1[32];
+    tmem_ld32_start(s_tm, r0);
+    tmem_ld32_start(s_tm + 32u, r1);
+    tmem_wait32(r0);
+    tmem_wait32(r1);
+    drop32<MASKED>(r0, MASKED ? allowed[0] : 0u);
+    drop32<MASKED>(r1, MASKED ? allowed[1] : 0u);
+    const float top = fmaxf(top32(r0), top32(r1)) * mul;
     bool ok = true;
     const bool raise = top > st.ref + kLazy;          // (ref = -inf: any finite score)
     if (first) {
         st.ref = top;
-    } else if (__any_sync(0xffffffffu, raise)) {
+    } else if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
         const float f = raise ? ex2(st.ref - top) : 1.0f;
         if (raise) st.ref = top;
         st.sum *= f;
-        ok = wait_acc();
-        tc::fence_after_sync();
-        for (int c = 0; c < o_cols; c += 16) {           // (few registers: the scores are live)
-            uint32_t o[16];
-            tmem_ld16(o_tm + (uint32_t)c, o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st16(o_tm + (uint32_t)c, o);
-        }
+        ok = scale_acc(f);
     }
     const float bias = kShift<BF16> - (st.ref == -CUDART_INF_F ? 0.0f : st.ref);
-    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t w[32];
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-            const float a = ex2(fmaf(__uint_as_float(r[64 * h + c]), mul, bias));
-            const float b = ex2(fmaf(__uint_as_float(r[64 * h + c + 1]), mul, bias));
-            sum[c & 2] += a;
-            sum[(c & 2) + 1] += b;
-            w[c >> 1] = pack2<BF16>(a, b);
-        }
-        tmem_st32(s_tm + 32u * (uint32_t)h, w);
-    }
-    st.sum += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    const uint64_t m2 = pair(mul, mul), b2 = pair(bias, bias);
+    uint64_t sum[2] = {0ull, 0ull};
+    weights32<BF16>(r0, m2, b2, s_tm, sum);
+    weights32<BF16>(r1, m2, b2, s_tm + 16u, sum);
+    const uint64_t s2 = add2(sum[0], sum[1]);
+    st.sum += __uint_as_float((uint32_t)s2) + __uint_as_float((uint32_t)(s2 >> 32));
     tmem_wait_st();
     tc::fence_before_sync();
     return ok;

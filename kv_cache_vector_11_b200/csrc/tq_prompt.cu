@@ -8,7 +8,7 @@
 // 128 / GP consecutive queries: grouped heads share every key tile that is
 // loaded, and the tiles cut by the causal edge are GP times fewer.  Key and
 // value tiles (128 keys) arrive by TMA into one ring of buffers, from the last
-// key tile to the first; one thread issues the MMAs, one softmax thread per row
+// key tile to the first; two threads issue the MMAs, one softmax thread per row
 // reads its scores from TMEM and writes the weights back over them (tq_fmha.cuh).
 //
 //  d <= 128: two row tiles; the tensor core works on one tile while the
@@ -19,7 +19,7 @@
 //
 // Values at keys that a row may not attend meet a zero weight, which a NaN or
 // an infinity would turn into NaN.  Such pairs exist only in the tiles at the
-// causal edge and at the sequence's end.  There two warps look over the value
+// causal edge and at the sequence's end.  There a warp looks over the value
 // tile before the second product: rows past the sequence are zeroed, and a
 // non-finite value inside it makes the CTA compute its rows again on the CUDA
 // cores, with the keys that a row attends and no others.
@@ -71,10 +71,11 @@ struct PaCfg {
     static constexpr int THREADS = 128 * NQ + 128;
     static constexpr int OFF_KV = NQ * NH * BUF;
     static constexpr int OFF_BAR = OFF_KV + STAGES * BUF;
-    // mbarriers: q, full[STAGES], empty[STAGES], s_full[2], p_full[2],
-    // o_done[2], scanned, drained; then the TMEM address, error and redo flags, the
-    // tile, and the sums of the search for it
-    static constexpr int N_BAR = 2 * STAGES + 9;
+    // mbarriers: q, full[STAGES], empty[STAGES], s_full[2][2], p_full[2][2],
+    // o_done[2][2], o_last[2], s_free[2], drained[2], scanned; then the
+    // TMEM address, error and redo flags, the tile, and the sums of the search
+    // for it
+    static constexpr int N_BAR = 2 * STAGES + 20;
     static constexpr int OFF_MISC = OFF_BAR + 8 * N_BAR;
     static constexpr int SMEM = OFF_MISC + 32 + 8 * (THREADS / 32) + 1024;   // + alignment of the base
     static_assert(SMEM <= 232448, "shared memory of a CTA");
@@ -115,6 +116,10 @@ __device__ __noinline__ void prompt_row(const PromptArgs & a, int64_t tok, int h
     for (int e = 0; e < E; ++e) from_f32(n > 0 ? o[e] / l : 0.0f, op + lane + 32 * e);
 }
 
+// Out of line: rare, and away from the softmax's instructions.
+template <int D>
+__device__ __noinline__ void scale_row(uint32_t o_tm, float f) { fm::rescale(o_tm, D, f); }
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(PaCfg<D>::THREADS, 1)
 prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap qmap,
@@ -130,7 +135,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t bar = sbase + (uint32_t)C::OFF_BAR;
     const uint32_t q_full = bar, full = bar + 8u, empty = full + 8u * ST, s_full = empty + 8u * ST,
-                   p_full = s_full + 16u, o_done = p_full + 16u, scanned = o_done + 16u, drained = scanned + 8u;
+                   p_full = s_full + 32u, o_done = p_full + 32u, o_last = o_done + 32u, s_free = o_last + 16u,
+                   drained = s_free + 16u, scanned = drained + 16u;
     uint32_t * s_tmem = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int * s_err = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
     volatile int * s_redo = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8);
@@ -201,15 +207,19 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             tc::mbar_init(q_full, 1);
             for (int i = 0; i < ST; ++i) {
                 tc::mbar_init(full + 8u * i, 1);
-                tc::mbar_init(empty + 8u * i, 1);
+                tc::mbar_init(empty + 8u * i, NQ == 1 ? 1 : slots);
             }
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 tc::mbar_init(s_full + 8u * i, 1);
                 tc::mbar_init(p_full + 8u * i, 128);
                 tc::mbar_init(o_done + 8u * i, 1);
             }
-            tc::mbar_init(scanned, 64);
-            tc::mbar_init(drained, 1);
+            for (int i = 0; i < 2; ++i) {
+                tc::mbar_init(o_last + 8u * i, 1);
+                tc::mbar_init(s_free + 8u * i, 1);
+                tc::mbar_init(drained + 8u * i, 1);
+            }
+            tc::mbar_init(scanned, 32);
         }
         if (warp == 0) tc::tmem_alloc(sbase + (uint32_t)C::OFF_MISC, 512);
         tc::fence_before_sync();
@@ -217,7 +227,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         tc::fence_after_sync();
     }
     const uint32_t tmem = n > 0 ? *s_tmem : 0u;
-    const int ctrl = warp - 4 * NQ;                       // 0: MMAs, 1: copies, 2 and 3: value scan
+    const int ctrl = warp - 4 * NQ;                       // 0 and 3: MMAs, 1: copies, 2: value scan
 
     if (n > 0 && ctrl == 1) {
         if (lane == 0) {
@@ -238,7 +248,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
 #pragma unroll 1
                     for (int h = 0; h < NH && ok; ++h, ++it) {
                         const int s = it % ST;
-                        if (it >= ST) ok = tc::mbar_wait(empty + 8u * s, (uint32_t)((it / ST - 1) & 1), fm::kWaitNs) && *s_err == 0;
+                        if (it >= ST) ok = fm::wait(empty + 8u * s, (uint32_t)((it / ST - 1) & 1));
                         if (!ok) break;
                         tc::mbar_arrive_expect_tx(full + 8u * s, (uint32_t)C::BUF);
                         for (int c = 0; c < SW; ++c)
@@ -249,113 +259,152 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             }
             if (!ok) *s_err = 1;
             // the last copy into every buffer lands before the CTA ends
-            tc::mbar_wait(q_full, 0u, fm::kWaitNs);
+            fm::wait(q_full, 0u);
             for (int t = max(0, it - ST); t < it; ++t)
-                tc::mbar_wait(full + 8u * (t % ST), (uint32_t)((t / ST) & 1), fm::kWaitNs);
+                fm::wait(full + 8u * (t % ST), (uint32_t)((t / ST) & 1));
         }
         __syncwarp();
-    } else if (n > 0 && ctrl == 0) {
-        if (lane == 0) {
-            constexpr uint32_t id_qk = fm::idesc(BF16, kTile, false), id_pv = fm::idesc(BF16, C::W, true);
-            bool ok = tc::mbar_wait(q_full, 0u, fm::kWaitNs);
-            auto wait_buf = [&](int it) {
-                return tc::mbar_wait(full + 8u * (it % ST), (uint32_t)((it / ST) & 1), fm::kWaitNs) && *s_err == 0;
-            };
-            auto buf = [&](int it) { return sbase + (uint32_t)(C::OFF_KV + (it % ST) * C::BUF); };
-            // scores of row tile i and the key half h at `it` into slot s
-            auto qk = [&](int i, int s, int h, int it) {
-                const uint32_t qa = sbase + (uint32_t)((i * NH + h) * C::BUF), kb = buf(it);
+    } else if (n > 0 && (ctrl == 0 || ctrl == 3)) {
+        // ---- MMAs, issued by two threads.  An MMA holds its thread about as long
+        // as the tensor core works on it, a wait or a commit costs some 100 cycles
+        // more; with two threads those of one overlap the products of the other
+        // (8192-token prompt, d = 128: 0.579 ms with one thread, MMA2 with two). ----
+        const int t = ctrl == 0 ? 0 : 1;
+        if (lane == 0 && (NQ == 1 || t < slots)) {
+            constexpr uint32_t id_qk = fm::idesc(BF16, kTile, false), id_qk64 = fm::idesc(BF16, 64, false), id_pv = fm::idesc(BF16, C::W, true);
+            const uint64_t kv_desc = tc::smem_desc_sw128(sbase + (uint32_t)C::OFF_KV);
+            const uint64_t v_desc = fm::smem_desc_sw128_mn(sbase + (uint32_t)C::OFF_KV, (uint32_t)C::SLICE);
+            // scores of row tile i and the columns h of the key tile in buffer b
+            // into slot s, keys from row `key` of the tile on
+            auto qk = [&](int i, int s, int h, uint32_t b, int key, uint32_t id) {
+                const uint64_t qd = fm::opaque(tc::smem_desc_sw128(sbase + (uint32_t)((i * NH + h) * C::BUF)));
+                const uint64_t kd = kv_desc + (uint64_t)(b * (uint32_t)(C::BUF >> 4) + 8u * (uint32_t)key);
 #pragma unroll
                 for (int ks = 0; ks < C::W / 16; ++ks) {
-                    const uint32_t off = (uint32_t)((ks >> 2) * C::SLICE + (ks & 3) * 32);
-                    tc::mma_bf16(tmem + (uint32_t)s * fm::kSlotCols, tc::smem_desc_sw128(qa + off),
-                                 tc::smem_desc_sw128(kb + off), id_qk, h > 0 || ks > 0 ? 1u : 0u);
+                    const uint64_t off = (uint64_t)(((ks >> 2) * C::SLICE + (ks & 3) * 32) >> 4);
+                    tc::mma_bf16(tmem + (uint32_t)s * fm::kSlotCols + (uint32_t)key, qd + off, kd + off, id, h > 0 || ks > 0 ? 1u : 0u);
                 }
             };
-            // weights in slot s times the value half h at `it` onto accumulator i
-            auto pv = [&](int i, int s, int h, int it, bool acc) {
-                const uint32_t vb = buf(it);
+            // weights of half g of slot s times the columns h of the value tile in
+            // buffer b onto accumulator i
+            auto pv = [&](int i, int s, int h, uint32_t b, int g, bool acc) {
+                const uint64_t vd = v_desc + (uint64_t)(b * (uint32_t)(C::BUF >> 4) + 512u * (uint32_t)g);
 #pragma unroll
-                for (int ks = 0; ks < kTile / 16; ++ks)
-                    fm::mma_ts(tmem + fm::kOutCol + (uint32_t)(i * D + h * C::W), tmem + (uint32_t)s * fm::kSlotCols + 8u * ks,
-                               fm::smem_desc_sw128_mn(vb + 2048u * ks, (uint32_t)C::SLICE), id_pv, acc || ks > 0 ? 1u : 0u);
+                for (int k = 0; k < 4; ++k)
+                    fm::mma_ts(tmem + fm::kOutCol + (uint32_t)(i * D + h * C::W),
+                               tmem + (uint32_t)s * fm::kSlotCols + (uint32_t)g * fm::kHalfCols + 8u * k, vd + 128u * k, id_pv,
+                               acc || k > 0 ? 1u : 0u);
             };
+            bool ok = fm::wait(q_full, 0u);
+            fm::Ring<ST> ring;                            // the next buffer
             if constexpr (NQ == 2) {
-                ok = ok && wait_buf(0);
+                // thread t: row tile t.  The scores of a half come behind the
+                // products that read the weights they overwrite.
+                const uint32_t sf = s_full + 16u * t, pf = p_full + 16u * t, od = o_done + 16u * t;
+                ok = ok && fm::wait(full, 0u);
                 if (ok) {
-                    for (int i = 0; i < slots; ++i) {
-                        qk(i, i, 0, 0);
-                        tc::commit(s_full + 8u * i);
+                    for (int g = 0; g < 2; ++g) {
+                        qk(t, t, 0, 0u, 64 * g, id_qk64);
+                        tc::commit(sf + 8u * g);
                     }
                     tc::commit(empty);
                 }
+                ring.step();
                 for (int j = 0; j < n && ok; ++j) {
-                    const int iv = 2 * j + 1, ik = 2 * j + 2;
-                    ok = wait_buf(iv) && (j >= n_edge || tc::mbar_wait(scanned, (uint32_t)(j & 1), fm::kWaitNs));
-                    for (int i = 0; i < slots && ok; ++i) {
-                        ok = tc::mbar_wait(p_full + 8u * i, (uint32_t)(j & 1), fm::kWaitNs) && *s_err == 0;
+                    const uint32_t v = ring.at, vp = ring.parity;
+                    ring.step();
+                    const uint32_t k = ring.at, kp = ring.parity;
+                    ring.step();
+                    const bool more = j + 1 < n;
+                    ok = fm::wait(full + 8u * v, vp);
+                    if (j < n_edge) ok = ok && fm::wait(scanned, (uint32_t)(j & 1));
+                    if (more) ok = ok && fm::wait(full + 8u * k, kp);
+                    ok = ok && fm::wait(pf, (uint32_t)(j & 1));
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    pv(t, t, 0, v, 0, j > 0);
+                    if (more) {
+                        qk(t, t, 0, k, 0, id_qk64);
+                        tc::commit(sf);
+                    }
+                    tc::commit(od);
+                    ok = fm::wait(pf + 8u, (uint32_t)(j & 1));
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    pv(t, t, 0, v, 1, true);
+                    if (more) {
+                        qk(t, t, 0, k, 64, id_qk64);
+                        tc::commit(sf + 8u);
+                        tc::commit(empty + 8u * k);
+                    }
+                    tc::commit(od + 8u);
+                    tc::commit(empty + 8u * v);
+                }
+                if (ok) tc::commit(o_last + 8u * t);
+            } else if (t == 0) {
+                // scores: slot j & 1 is free again behind the products of tile j - 2
+                for (int j = 0; j < n && ok; ++j) {
+                    if (j > 1) ok = fm::wait(s_free + 8u * (j & 1), (uint32_t)(((j >> 1) - 1) & 1));
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+                        ok = ok && fm::wait(full + 8u * ring.at, ring.parity);
                         if (!ok) break;
                         tc::fence_after_sync();
-                        pv(i, i, 0, iv, j > 0);
-                        tc::commit(o_done + 8u * i);
-                        if (i == slots - 1) tc::commit(empty + 8u * (iv % ST));
-                        if (j + 1 < n) {
-                            if (i == 0) ok = wait_buf(ik);
-                            if (!ok) break;
-                            qk(i, i, 0, ik);
-                            tc::commit(s_full + 8u * i);
-                            if (i == slots - 1) tc::commit(empty + 8u * (ik % ST));
-                        }
+                        qk(0, j & 1, h, ring.at, 0, id_qk);
+                        tc::commit(empty + 8u * ring.at);
+                        ring.step();
                     }
+                    for (int h = 0; h < NH; ++h) ring.step();                 // (the values)
+                    for (int g = 0; g < 2 && ok; ++g) tc::commit(s_full + 8u * (2 * (j & 1) + g));
                 }
             } else {
-                auto scores = [&](int j) {
-                    for (int h = 0; h < NH && ok; ++h) {
-                        const int it = 2 * NH * j + h;
-                        ok = wait_buf(it);
-                        if (!ok) return;
-                        tc::fence_after_sync();
-                        qk(0, j & 1, h, it);
-                        tc::commit(empty + 8u * (it % ST));
-                    }
-                    tc::commit(s_full + 8u * (j & 1));
-                };
-                if (ok) scores(0);
+                // products
                 for (int j = 0; j < n && ok; ++j) {
-                    if (j + 1 < n) scores(j + 1);
-                    ok = ok && (j >= n_edge || tc::mbar_wait(scanned, (uint32_t)(j & 1), fm::kWaitNs)) &&
-                         tc::mbar_wait(p_full + 8u * (j & 1), (uint32_t)((j >> 1) & 1), fm::kWaitNs) && *s_err == 0;
-                    for (int h = 0; h < NH && ok; ++h) {
-                        const int it = 2 * NH * j + NH + h;
-                        ok = wait_buf(it);
+                    for (int h = 0; h < NH; ++h) ring.step();                 // (the keys)
+                    uint32_t b[NH];
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+                        b[h] = ring.at;
+                        ok = ok && fm::wait(full + 8u * ring.at, ring.parity);
+                        ring.step();
+                    }
+                    if (j < n_edge) ok = ok && fm::wait(scanned, (uint32_t)(j & 1));
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        ok = ok && fm::wait(p_full + 8u * (2 * (j & 1) + g), (uint32_t)((j >> 1) & 1));
                         if (!ok) break;
                         tc::fence_after_sync();
-                        pv(0, j & 1, h, it, j > 0);
-                        tc::commit(empty + 8u * (it % ST));
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) {
+                            pv(0, j & 1, h, b[h], g, j > 0 || g > 0);
+                            if (g == 1) tc::commit(empty + 8u * b[h]);
+                        }
+                        tc::commit(o_done + 8u * g);
                     }
-                    if (ok) tc::commit(o_done);
+                    if (ok) tc::commit(s_free + 8u * (j & 1));
                 }
+                if (ok) tc::commit(o_last);
             }
             if (!ok) {
                 // the MMAs in flight end before their columns are freed
                 *s_err = 1;
-                tc::commit(drained);
-                tc::mbar_wait(drained, 0u, fm::kWaitNs);
+                tc::commit(drained + 8u * t);
+                fm::wait(drained + 8u * t, 0u);
             }
         }
         __syncwarp();
-    } else if (n > 0 && ctrl >= 2) {
-        // values of the edge tiles: thread t looks over rows t and t + 64
-        const int t = tid - 128 * NQ - 64;
+    } else if (n > 0 && ctrl == 2) {
+        // values of the edge tiles: thread t looks over every 32nd row from t
+        const int t = lane;
         bool ok = true;
         for (int j = 0; j < n_edge && ok; ++j) {
             bool bad = false;
             for (int h = 0; h < NH && ok; ++h) {
                 const int it = 2 * NH * j + NH + h;
-                ok = tc::mbar_wait(full + 8u * (it % ST), (uint32_t)((it / ST) & 1), fm::kWaitNs) && *s_err == 0;
+                ok = fm::wait(full + 8u * (it % ST), (uint32_t)((it / ST) & 1));
                 if (!ok) break;
                 unsigned char * vb = smem + C::OFF_KV + (it % ST) * C::BUF;
-                for (int r = t; r < kTile; r += 64) {
+                for (int r = t; r < kTile; r += 32) {
                     uint32_t non = 0u;
                     for (int c = 0; c < C::W / 8; ++c) {
                         const uint4 u = *reinterpret_cast<const uint4 *>(vb + (c >> 3) * C::SLICE + r * 128 + 16 * ((c & 7) ^ (r & 7)));
@@ -374,8 +423,9 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             }
             if (bad) *s_redo = 1;
             // one tile ahead of the products at most: `scanned` must not pass
-            // a phase that the issuing thread has not waited for
-            if (j > 0) ok = ok && tc::mbar_wait(o_done, (uint32_t)((j - 1) & 1), fm::kWaitNs);
+            // a phase that an issuing thread has not waited for
+            for (int i = 0; i < slots && j > 0; ++i)
+                ok = ok && fm::wait(o_done + 8u * (2 * i + 1), (uint32_t)((j - 1) & 1));
             if (!ok) {
                 *s_err = 1;
                 break;
@@ -399,31 +449,43 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             bool ok = true;
             for (int j = 0; j < n && ok; ++j) {
                 const int slot = NQ == 2 ? i : (j & 1), use = NQ == 2 ? j : (j >> 1);
-                ok = tc::mbar_wait(s_full + 8u * slot, (uint32_t)(use & 1), fm::kWaitNs) && *s_err == 0;
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc::fence_after_sync();
                 const uint32_t s_tm = lane_tm + (uint32_t)slot * fm::kSlotCols;
-                auto wait_acc = [&] { return tc::mbar_wait(o_done + 8u * i, (uint32_t)((j - 1) & 1), fm::kWaitNs); };
+                uint32_t allowed[4];
                 if (j < n_edge) {
                     const int left = lim - (n - 1 - j) * kTile;           // columns of this tile to keep
-                    uint32_t allowed[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         const int c = left - 32 * x;
                         allowed[x] = c >= 32 ? 0xFFFFFFFFu : c <= 0 ? 0u : (1u << c) - 1u;
                     }
-                    ok = fm::softmax_tile<BF16, true>(s_tm, o_tm, D, j == 0, mul, allowed, st, wait_acc);
-                } else {
-                    ok = fm::softmax_tile<BF16, false>(s_tm, o_tm, D, j == 0, mul, nullptr, st, wait_acc);
                 }
-                tc::mbar_arrive(p_full + 8u * slot);
+#pragma unroll 1
+                for (int g = 0; g < 2 && ok; ++g) {
+                    // (the scores that follow in this half wait for these weights)
+                    ok = fm::wait(s_full + 8u * (2 * slot + g), (uint32_t)(use & 1));
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    // products so far: the second half of the tile before -- d = 256
+                    // had the scores of this tile behind those of tile j - 2 at the
+                    // latest -- then, in this half 1, those of half 0
+                    auto scale_acc = [&](float f) {
+                        bool r = j == 0 || fm::wait(o_done + 8u * (2 * i + 1), (uint32_t)((j - 1) & 1));
+                        if (g == 1) r = r && fm::wait(o_done + 8u * (2 * i), (uint32_t)(j & 1));
+                        scale_row<D>(o_tm, f);
+                        return r;
+                    };
+                    const uint32_t half = s_tm + (uint32_t)g * fm::kHalfCols;
+                    if (j < n_edge) {
+                        const uint32_t al[2] = {g == 0 ? allowed[0] : allowed[2], g == 0 ? allowed[1] : allowed[3]};
+                        ok = fm::softmax_half<BF16, true>(half, j + g == 0, mul, al, st, scale_acc);
+                    } else {
+                        ok = fm::softmax_half<BF16, false>(half, j + g == 0, mul, nullptr, st, scale_acc);
+                    }
+                    tc::mbar_arrive(p_full + 8u * (2 * slot + g));
+                }
             }
-            // the last product (d = 256: the scores of a tile come before the
-            // products of the one in front of it, so that one is waited for first:
-            // a wait may be one phase ahead of the barrier, not two)
-            if (NQ == 1 && n > 1) ok = ok && tc::mbar_wait(o_done, (uint32_t)(n & 1), fm::kWaitNs);
-            ok = ok && tc::mbar_wait(o_done + 8u * i, (uint32_t)((n - 1) & 1), fm::kWaitNs);
+            ok = ok && fm::wait(o_last + 8u * i, 0u);
             if (!ok) *s_err = 1;
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {

@@ -18,7 +18,7 @@
 // the rows' own slots, so a row has one own slot and one more per further CTA.
 //
 // In the CTA four warps unpack codes into the swizzled operand tiles (shared
-// memory, a ring of buffers), one thread issues the MMAs, one softmax thread
+// memory, a ring of buffers), two threads issue the MMAs, one softmax thread
 // per row turns scores into weights (tq_fmha.cuh).  Which rows share a CTA:
 //   PAIR:   two row tiles (256 rows) against the same key tile: unpacking is
 //           paid once for both, the tensor core works on one while the softmax
@@ -323,13 +323,14 @@ __device__ __forceinline__ uint4 lookup8(uint32_t x, const uint32_t * tab, __hal
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// One row of an operand buffer: NB blocks of BITS words, norms two to a word.
+// One side of a row of an operand buffer: NB blocks of BITS words, their norms
+// in one word.
 template <int BITS, int NB>
-__device__ __forceinline__ void unpack_row(const uint32_t * w, const uint32_t * norms, const uint32_t * tab,
-                                           unsigned char * dst, int swz) {
+__device__ __forceinline__ void unpack_row(const uint32_t * w, uint32_t norms, const uint32_t * tab, unsigned char * dst,
+                                           int side, int swz) {
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk) {
-        const uint32_t nn = __byte_perm(norms[blk >> 1], 0u, (blk & 1) ? 0x3232 : 0x1010);
+        const uint32_t nn = __byte_perm(norms, 0u, blk ? 0x3232 : 0x1010);
         const __half2 norm = *reinterpret_cast<const __half2 *>(&nn);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -350,8 +351,9 @@ __device__ __forceinline__ void unpack_row(const uint32_t * w, const uint32_t * 
                 x = (x | (x << 4)) & 0x0F0F0F0Fu;
                 x = (x | (x << 2)) & 0x33333333u;
             }
-            const int c = 4 * blk + k;                   // 16-byte chunk of the row
-            *reinterpret_cast<uint4 *>(dst + (c >> 3) * (kTile * 128) + 16 * ((c & 7) ^ swz)) = lookup8<BITS == 4>(x, tab, norm);
+            // 16-byte chunk of the row: two blocks of a side fill a slice, one block half of it
+            const int c = NB == 2 ? 4 * blk + k : 4 * side + k;
+            *reinterpret_cast<uint4 *>(dst + (NB == 2 ? side * (kTile * 128) : 0) + 16 * (c ^ swz)) = lookup8<BITS == 4>(x, tab, norm);
         }
     }
 }
@@ -390,25 +392,26 @@ struct TaCfg {
     static constexpr int LEAD = MODE == PAIR ? 0 : 1;    // tiles that the keys are ahead of the values
     static constexpr int OFF_RING = QT * NH * BUF;
     static constexpr int STAGES = (192 * 1024 - OFF_RING) / BUF < 8 ? (192 * 1024 - OFF_RING) / BUF : 8;
-    static constexpr int THREADS = 128 * (WGS + 2);      // softmax, unpacking, MMAs
-    // packed rows on their way: codes as 4 chunks x 128 threads x CHUNK bytes,
-    // then the norms and the other norms, 2 NB bytes a thread
-    static constexpr int CHUNK = 4 * NB, NORMS = 2 * NB;
+    static constexpr int THREADS = 128 * (WGS + 3);      // softmax, two warpgroups of unpacking, the issuing threads
+    // packed rows on their way, two threads a row: codes as 4 chunks x 256
+    // threads x CHUNK bytes, then one word of norms and one of the other norms
+    static constexpr int NBT = NB / 2;                   // blocks of a thread
+    static constexpr int CHUNK = 4 * NBT;
     static constexpr int OFF_PACKED = OFF_RING + STAGES * BUF;
-    static constexpr int PACKED = kTile * (4 * CHUNK + 2 * NORMS);
-    // mbarriers: full[STAGES], empty[STAGES], s_full[2], p_full[2], o_done[2],
-    // o_free[2], q_full, q_free, drained
+    static constexpr int PACKED = 2 * kTile * (4 * CHUNK + 8);
+    // mbarriers: full[STAGES], empty[STAGES], s_full[2][2], p_full[2][2],
+    // o_done[2][2], o_last[2], o_free[2], s_free[2], drained[2], q_full, q_free
     static constexpr int OFF_BAR = OFF_PACKED + 3 * PACKED;
-    static constexpr int N_BAR = 2 * STAGES + 11;
-    static constexpr int OFF_BAD = (OFF_BAR + 8 * N_BAR + 15) / 16 * 16;    // 8 tiles x 128 bits: keys with a bad norm
-    static constexpr int OFF_MISC = OFF_BAD + 128;                           // TMEM address, error flag, first request
+    static constexpr int N_BAR = 2 * STAGES + 22;
+    static constexpr int OFF_BAD = (OFF_BAR + 8 * N_BAR + 15) / 16 * 16;    // 8 tiles x two threads a row x 128 bits: keys with a bad norm
+    static constexpr int OFF_MISC = OFF_BAD + 256;                           // TMEM address, error flag, first request
     static constexpr int SMEM = OFF_MISC + 16 + 1024;                       // + alignment of the base
     static_assert(SMEM <= 232448, "shared memory of a CTA");
-    // registers a thread: the launch's share is 128 (512 threads) or 168 (384)
-    static constexpr int R_SOFTMAX = WGS == 2 ? 192 : 240;
-    static constexpr int R_UNPACK = WGS == 2 ? 80 : 168;
-    static constexpr int R_MMA = WGS == 2 ? 48 : 96;
-    static_assert(WGS * R_SOFTMAX + R_UNPACK + R_MMA <= (WGS == 2 ? 512 : 504), "no more than the launch holds");
+    // registers a thread: 96 at launch (640 threads) or 128 (512)
+    static constexpr int R_SOFTMAX = WGS == 2 ? 136 : 168;
+    static constexpr int R_UNPACK = WGS == 2 ? 80 : 120;
+    static constexpr int R_MMA = WGS == 2 ? 48 : 104;
+    static_assert(WGS * R_SOFTMAX + 2 * R_UNPACK + R_MMA <= (WGS == 2 ? 480 : 512), "no more than the launch holds");
 };
 
 template <int N>
@@ -433,8 +436,8 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
     unsigned char * smem = smem_raw + (sbase - raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t full = sbase + (uint32_t)C::OFF_BAR, empty = full + 8u * ST, s_full = empty + 8u * ST,
-                   p_full = s_full + 16u, o_done = p_full + 16u, o_free = o_done + 16u, q_full = o_free + 16u,
-                   q_free = q_full + 8u, drained = q_free + 8u;
+                   p_full = s_full + 32u, o_done = p_full + 32u, o_last = o_done + 32u, o_free = o_last + 16u,
+                   s_free = o_free + 16u, drained = s_free + 16u, q_full = drained + 16u, q_free = q_full + 8u;
     volatile uint32_t * s_bad = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_BAD);
     uint32_t * s_tmem = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int * s_err = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
@@ -442,18 +445,22 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
 
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
-            tc::mbar_init(full + 8u * i, 4);
-            tc::mbar_init(empty + 8u * i, 1);
+            tc::mbar_init(full + 8u * i, 8);
+            tc::mbar_init(empty + 8u * i, MODE == PAIR ? 2 : 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             tc::mbar_init(s_full + 8u * i, 1);
             tc::mbar_init(p_full + 8u * i, 128);
             tc::mbar_init(o_done + 8u * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(o_last + 8u * i, 1);
             tc::mbar_init(o_free + 8u * i, 128);
+            tc::mbar_init(s_free + 8u * i, 1);
+            tc::mbar_init(drained + 8u * i, 1);
         }
         tc::mbar_init(q_full, 1);
-        tc::mbar_init(q_free, 1);
-        tc::mbar_init(drained, 1);
+        tc::mbar_init(q_free, MODE == WIDE ? 1 : 2);
         *s_err = 0;
     }
     if (warp == 0) tc::tmem_alloc(sbase + (uint32_t)C::OFF_MISC, 512);
@@ -471,137 +478,218 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
     it.start(a, *s_first);
     Part p;
 
-    if (warp >= 4 * (WGS + 1)) {
-        // ---- MMAs ----
+    if (warp >= 4 * (WGS + 2)) {
         regs_down<C::R_MMA>();
-        if (warp == 4 * (WGS + 1) && lane == 0) {
-            constexpr uint32_t id_qk = fm::idesc(false, kTile, false), id_pv = fm::idesc(false, C::W, true);
+        // ---- MMAs, issued by two threads (as in the prompt kernel): PAIR and
+        // STREAM one per score slot, WIDE one for the scores and one for the
+        // products; a third warp loads the row tiles ----
+        const int t = warp - 4 * (WGS + 2);
+        if (t == 2 && lane == 0) {
             bool ok = true;
-            int ring = 0, parts = 0, wide = 0;               // buffers, parts, (WIDE) tiles so far
-            int left[2] = {0, 0};          // finished parts of a softmax warpgroup
-            int slot_used[2] = {0, 0};                       // tiles of a score slot
-            auto wait = [&](uint32_t bar, int phase) { return tc::mbar_wait(bar, (uint32_t)(phase & 1), fm::kWaitNs) && *s_err == 0; };
-            // scores of row tile t against the next key tile, into slot s
-            auto qk = [&](int t, int s, int at) {
-#pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                    const uint32_t qa = sbase + (uint32_t)((t * NH + h) * C::BUF);
-                    const uint32_t kb = sbase + (uint32_t)(C::OFF_RING + ((at + h) % ST) * C::BUF);
-#pragma unroll
-                    for (int ks = 0; ks < C::W / 16; ++ks) {
-                        const uint32_t off = (uint32_t)((ks >> 2) * C::SLICE + (ks & 3) * 32);
-                        tc::mma_bf16(tmem + (uint32_t)s * fm::kSlotCols, tc::smem_desc_sw128(qa + off),
-                                     tc::smem_desc_sw128(kb + off), id_qk, h > 0 || ks > 0 ? 1u : 0u);
-                    }
-                }
-                tc::commit(s_full + 8u * s);
-            };
-            // weights of slot s times the value tile, onto accumulator w
-            auto pv = [&](int w, int s, int at, bool acc) {
-#pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                    const uint32_t vb = sbase + (uint32_t)(C::OFF_RING + ((at + h) % ST) * C::BUF);
-#pragma unroll
-                    for (int ks = 0; ks < kTile / 16; ++ks)
-                        fm::mma_ts(tmem + fm::kOutCol + (uint32_t)(w * D + h * C::W), tmem + (uint32_t)s * fm::kSlotCols + 8u * ks,
-                                   fm::smem_desc_sw128_mn(vb + 2048u * ks, (uint32_t)C::SLICE), id_pv, acc || ks > 0 ? 1u : 0u);
-                }
-                tc::commit(o_done + 8u * w);
-            };
-            auto wait_tile = [&](int at) {                   // its buffers are written
-                bool r = true;
-                for (int h = 0; h < NH && r; ++h) r = wait(full + 8u * ((at + h) % ST), (at + h) / ST);
-                tc::fence_after_sync();
-                return r;
-            };
-            auto release = [&](int at) {
-                for (int h = 0; h < NH; ++h) tc::commit(empty + 8u * ((at + h) % ST));
-            };
-            // softmax warpgroup w has written the weights in slot s; before the
-            // first product of a part its accumulator must have been read
-            auto wait_weights = [&](int w, int s, bool first) {
-                bool r = wait(p_full + 8u * s, slot_used[s]);
-                if (r && first && left[w] > 0) r = wait(o_free + 8u * w, left[w] - 1);
-                ++slot_used[s];
-                tc::fence_after_sync();
-                return r;
-            };
-            while (ok && it.next(a, p)) {
-                // the row tiles
-                if (parts > 0) ok = wait(q_free, parts - 1);
+            for (int part = 0; ok && it.next(a, p); ++part) {
+                if (part > 0) ok = fm::wait(q_free, (uint32_t)((part - 1) & 1));
                 if (!ok) break;
                 const int tiles = MODE == PAIR && p.rows > kTile ? 2 : 1;
                 tc::mbar_arrive_expect_tx(q_full, (uint32_t)(tiles * (D / 64) * C::SLICE));
-                for (int t = 0; t < tiles; ++t)
+                for (int i = 0; i < tiles; ++i)
                     for (int c = 0; c < D / 64; ++c)
-                        tc::tma_load_2d(sbase + (uint32_t)((t * (D / 64) + c) * C::SLICE), &qmap, 64 * c,
-                                        (int)p.row_id + t * kTile, q_full);
-                ok = tc::mbar_wait(q_full, (uint32_t)(parts & 1), fm::kWaitNs);
-                ++parts;
-                if constexpr (MODE == PAIR) {
-                    ok = ok && wait_tile(ring);
-                    if (!ok) break;
-                    for (int t = 0; t < tiles; ++t) qk(t, t, ring);
-                    release(ring++);
-                    if (p.tiles == 1) tc::commit(q_free);
-                    for (int j = 0; j < p.tiles && ok; ++j) {
-                        const int iv = ring, ik = ring + 1;
-                        ok = wait_tile(iv);
-                        for (int t = 0; t < tiles && ok; ++t) {
-                            ok = wait_weights(t, t, j == 0);
-                            if (!ok) break;
-                            pv(t, t, iv, j > 0);
-                            if (t == tiles - 1) release(iv);
-                            if (j + 1 < p.tiles) {
-                                if (t == 0) ok = wait_tile(ik);
-                                if (!ok) break;
-                                qk(t, t, ik);
-                                if (t == tiles - 1) release(ik);
+                        tc::tma_load_2d(sbase + (uint32_t)((i * (D / 64) + c) * C::SLICE), &qmap, 64 * c,
+                                        (int)p.row_id + i * kTile, q_full);
+                // (also before this thread ends)
+                ok = fm::wait(q_full, (uint32_t)(part & 1));
+            }
+            if (!ok) *s_err = 1;
+        } else if (t < 2 && lane == 0) {
+            constexpr uint32_t id_qk = fm::idesc(false, kTile, false), id_qk64 = fm::idesc(false, 64, false),
+                               id_pv = fm::idesc(false, C::W, true);
+            const uint64_t ring_desc = tc::smem_desc_sw128(sbase + (uint32_t)C::OFF_RING);
+            const uint64_t v_desc = fm::smem_desc_sw128_mn(sbase + (uint32_t)C::OFF_RING, (uint32_t)C::SLICE);
+            // scores of row tile i and the columns h of the key tile in buffer b
+            // into slot s, keys from row `key` of the tile on
+            auto qk = [&](int i, int s, int h, uint32_t b, int key, uint32_t id) {
+                const uint64_t qd = fm::opaque(tc::smem_desc_sw128(sbase + (uint32_t)((i * NH + h) * C::BUF)));
+                const uint64_t kd = ring_desc + (uint64_t)(b * (uint32_t)(C::BUF >> 4) + 8u * (uint32_t)key);
+#pragma unroll
+                for (int ks = 0; ks < C::W / 16; ++ks) {
+                    const uint64_t off = (uint64_t)(((ks >> 2) * C::SLICE + (ks & 3) * 32) >> 4);
+                    tc::mma_bf16(tmem + (uint32_t)s * fm::kSlotCols + (uint32_t)key, qd + off, kd + off, id, h > 0 || ks > 0 ? 1u : 0u);
+                }
+            };
+            // weights of half g of slot s times the columns h of the value tile in
+            // buffer b onto accumulator w
+            auto pv = [&](int w, int s, int h, uint32_t b, int g, bool acc) {
+                const uint64_t vd = v_desc + (uint64_t)(b * (uint32_t)(C::BUF >> 4) + 512u * (uint32_t)g);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    fm::mma_ts(tmem + fm::kOutCol + (uint32_t)(w * D + h * C::W),
+                               tmem + (uint32_t)s * fm::kSlotCols + (uint32_t)g * fm::kHalfCols + 8u * k, vd + 128u * k, id_pv,
+                               acc || k > 0 ? 1u : 0u);
+            };
+            fm::Ring<ST> ring;                               // the next buffer
+            bool ok = true;
+            uint32_t use = 0, finished = 0;                  // key tiles and parts of this thread so far
+            uint32_t sf = s_full + 16u * t, pf = p_full + 16u * t, od = o_done + 16u * t;
+            for (int part = 0; ok && it.next(a, p); ++part) {
+                // (every part in turn, also one that this thread has no share in)
+                ok = fm::wait(q_full, (uint32_t)(part & 1));
+                if (!ok) break;
+                if constexpr (MODE != WIDE) {
+                    // Slot t: PAIR row tile t against every key tile; STREAM the one row
+                    // tile against the key tiles t, t + 2, ...; the buffers between are
+                    // the other thread's.  No buffer is filled twice in front of a
+                    // thread that skips some: the ring is longer than what it skips.
+                    const bool takes = MODE == PAIR ? t * kTile < p.rows : t < p.tiles;
+                    const int i = MODE == PAIR ? t : 0, stride = MODE == PAIR ? 1 : 2;
+                    // ring positions: PAIR K0 V0 K1 V1 ..; STREAM K0 K1 V0 K2 V1 ..
+                    fm::Ring<ST> next = ring;
+                    for (int x = 0; x < 2 * p.tiles % (2 * ST); ++x) next.step();     // (whole turns change nothing)
+                    if (!takes) {
+                        if constexpr (MODE == PAIR) {
+                            for (int x = 0; x < 2 * p.tiles && ok; ++x) {
+                                ok = fm::wait(full + 8u * ring.at, ring.parity);
+                                tc::mbar_arrive(empty + 8u * ring.at);
+                                ring.step();
                             }
                         }
-                        if (j + 2 == p.tiles) tc::commit(q_free);
-                        ring += j + 1 < p.tiles ? 2 : 1;
+                        ring = next;
+                        tc::mbar_arrive(q_free);
+                        continue;
                     }
-                    for (int t = 0; t < tiles; ++t) ++left[t];
-                } else {
-                    // key tile j is ahead of value tile j - 1
-                    auto scores = [&](int j) {
-                        const int s = MODE == STREAM ? j & 1 : (wide + j) & 1;
-                        if (!wait_tile(ring)) return false;
-                        qk(0, s, ring);
-                        release(ring);
-                        ring += NH;
-                        if (j + 1 == p.tiles) tc::commit(q_free);
-                        return true;
-                    };
-                    ok = ok && scores(0) && (p.tiles < 2 || scores(1));
-                    for (int j = 0; j < p.tiles && ok; ++j) {
-                        const int w = MODE == STREAM ? j & 1 : 0, s = MODE == STREAM ? w : (wide + j) & 1;
-                        const bool first = j < WGS;
-                        ok = wait_weights(w, s, first) && wait_tile(ring);
+                    if (MODE == STREAM && t == 1) ring.step();
+                    fm::Ring<ST> kr = ring, vr = ring;
+                    if (MODE == PAIR) vr.step();
+                    else
+                        for (int x = 0; x < (t == 0 ? (p.tiles > 1 ? 2 : 1) : (p.tiles > 2 ? 3 : 2)); ++x) vr.step();
+                    ok = fm::wait(full + 8u * kr.at, kr.parity);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    for (int g = 0; g < 2; ++g) {
+                        qk(i, t, 0, kr.at, 64 * g, id_qk64);
+                        tc::commit(sf + 8u * g);
+                    }
+                    tc::commit(empty + 8u * kr.at);
+                    bool first = true;
+                    for (int j = MODE == STREAM ? t : 0; j < p.tiles; j += stride) {
+                        const bool more = j + stride < p.tiles;
+                        if (!more) tc::commit(q_free);       // (behind the part's last scores)
+                        // the next key tile and this value tile
+                        if (MODE == PAIR) {
+                            kr.step();
+                            kr.step();
+                        } else {
+                            // K(j + 2) is 4 on from K(j), or 3 from K(0)
+                            for (int x = 0; x < (j == 0 ? 3 : 4); ++x) kr.step();
+                        }
+                        ok = fm::wait(full + 8u * vr.at, vr.parity);
+                        if (more) ok = ok && fm::wait(full + 8u * kr.at, kr.parity);
+                        // the accumulator of the part before has been read
+                        if (first && finished > 0) ok = ok && fm::wait(o_free + 8u * t, (finished - 1) & 1u);
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            ok = ok && fm::wait(pf + 8u * g, use & 1u);
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            pv(t, t, 0, vr.at, g, !first || g > 0);
+                            if (more) {
+                                qk(i, t, 0, kr.at, 64 * g, id_qk64);
+                                tc::commit(sf + 8u * g);
+                            }
+                            tc::commit(od + 8u * g);
+                        }
                         if (!ok) break;
-                        pv(w, s, ring, !first);
-                        release(ring);
-                        ring += NH;
-                        if (j + 2 < p.tiles) ok = scores(j + 2);
+                        tc::commit(empty + 8u * vr.at);
+                        if (more) tc::commit(empty + 8u * kr.at);
+                        first = false;
+                        ++use;
+                        if (MODE == PAIR) {
+                            vr.step();
+                            vr.step();
+                        } else {
+                            // V(j + 2) is 4 on from V(j); the last value tile is right
+                            // behind the one before it
+                            for (int x = 0; x < (j + 3 == p.tiles ? 3 : 4); ++x) vr.step();
+                        }
                     }
-                    wide += p.tiles;
-                    for (int w = 0; w < WGS; ++w)
-                        if (p.tiles > w) ++left[w];
+                    if (!ok) break;
+                    tc::commit(o_last + 8u * t);
+                    ++finished;
+                    ring = next;
+                } else {
+                    // ring positions: K0 K1 V0 K2 V1 .., two buffers each
+                    if (t == 0) {
+                        // the last value tile of the part before is in: no buffer is then
+                        // filled twice in front of this thread
+                        for (int j = 0; j < p.tiles && ok; ++j, ++use) {
+                            // slot use & 1 is free behind the products of two tiles before
+                            if (use > 1) ok = fm::wait(s_free + 8u * (use & 1u), ((use >> 1) - 1) & 1u);
+#pragma unroll
+                            for (int h = 0; h < NH; ++h) {
+                                ok = ok && fm::wait(full + 8u * ring.at, ring.parity);
+                                if (!ok) break;
+                                tc::fence_after_sync();
+                                qk(0, (int)(use & 1u), h, ring.at, 0, id_qk);
+                                tc::commit(empty + 8u * ring.at);
+                                ring.step();
+                            }
+                            if (!ok) break;
+                            for (int g = 0; g < 2; ++g) tc::commit(s_full + 8u * (2 * (use & 1u) + g));
+                            if (j + 1 == p.tiles) tc::commit(q_free);
+                            // over V(j - 1); behind the last keys over V(j) too
+                            for (int v = (j > 0) + (j + 1 == p.tiles); v > 0; --v)
+                                for (int h = 0; h < NH; ++h) {
+                                    ok = ok && fm::wait(full + 8u * ring.at, ring.parity);
+                                    ring.step();
+                                }
+                        }
+                    } else {
+                        for (int h = 0; h < NH; ++h) ring.step();                    // K(0)
+                        for (int j = 0; j < p.tiles && ok; ++j, ++use) {
+                            if (j + 1 < p.tiles)
+                                for (int h = 0; h < NH; ++h) ring.step();            // K(j + 1)
+                            // (the weights are there, so the buffers in front of V(j) are filled)
+                            ok = fm::wait(p_full + 16u * (use & 1u), (use >> 1) & 1u);
+                            uint32_t b[NH];
+#pragma unroll
+                            for (int h = 0; h < NH; ++h) {
+                                b[h] = ring.at;
+                                ok = ok && fm::wait(full + 8u * ring.at, ring.parity);
+                                ring.step();
+                            }
+                            if (j == 0 && finished > 0) ok = ok && fm::wait(o_free, (finished - 1) & 1u);
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                if (g == 1) ok = ok && fm::wait(p_full + 16u * (use & 1u) + 8u, (use >> 1) & 1u);
+                                if (!ok) break;
+                                tc::fence_after_sync();
+#pragma unroll
+                                for (int h = 0; h < NH; ++h) {
+                                    pv(0, (int)(use & 1u), h, b[h], g, j > 0 || g > 0);
+                                    if (g == 1) tc::commit(empty + 8u * b[h]);
+                                }
+                                tc::commit(o_done + 8u * g);
+                            }
+                            if (ok) tc::commit(s_free + 8u * (use & 1u));
+                        }
+                        if (!ok) break;
+                        tc::commit(o_last);
+                        ++finished;
+                    }
                 }
             }
             if (!ok) {
                 // the MMAs in flight end before their columns are freed
                 *s_err = 1;
-                tc::commit(drained);
-                tc::mbar_wait(drained, 0u, fm::kWaitNs);
+                tc::commit(drained + 8u * t);
+                fm::wait(drained + 8u * t, 0u);
             }
         }
         __syncwarp();
     } else if (warp >= 4 * WGS) {
-        // ---- unpacking: thread r has row r of every buffer ----
-        if constexpr (WGS == 2) regs_down<C::R_UNPACK>();
-        const int r = tid - 128 * WGS;
+        // ---- unpacking: two threads have row r of every buffer, half its blocks
+        // each (one thread a row leaves a scheduler with one unpacking warp, which
+        // waits for its own results: 8 x 128K ONETHREAD ms, with two TWOTHREADS) ----
+        regs_down<C::R_UNPACK>();
+        const int u = tid - 128 * WGS, r = u & (kTile - 1), side = u >> 7;
         // items of a part, in the order that the MMAs take them: step j has the
         // key tile j and the value tile j - LEAD
         int step = 0, half = 0, what = 0;
@@ -615,7 +703,7 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
         };
         auto fetch_ahead = [&](int tile) {
             const int t0 = tile * kTile + r;
-            if ((r & 15) != 0 || t0 >= p.rq.len) return;
+            if ((u & 15) != 0 || u >= kTile || t0 >= p.rq.len) return;
             const int pg = min(max(ahead, 0), a.n_pages - 1);
             const int64_t row = (((int64_t)pg * a.n_kv_heads + p.hk) << a.page_shift) + (t0 & ((1 << a.page_shift) - 1));
             auto pre = [](const void * ptr, uint32_t bytes) {
@@ -644,16 +732,16 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
             int pg = 0;
             if (live) pg = min(max(__ldg(a.table + (int64_t)p.b * a.max_pages + (t >> a.page_shift)), 0), a.n_pages - 1);
             const int64_t row = live ? (((int64_t)pg * a.n_kv_heads + p.hk) << a.page_shift) + (t & ((1 << a.page_shift) - 1)) : 0;
-            const uint32_t * c = (what == 0 ? a.k_codes : a.v_codes) + row * (D / 32 * bits) + half * (NB * bits);
+            const uint32_t * c = (what == 0 ? a.k_codes : a.v_codes) + row * (D / 32 * bits) + half * (NB * bits) + side * (C::NBT * bits);
             const uint32_t dst = packed + (uint32_t)(slot * C::PACKED);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (i < bits) copy_or_zero<C::CHUNK>(dst + (uint32_t)((i * kTile + r) * C::CHUNK), c + i * NB, live);
-            const uint16_t * kn = a.k_norms + row * (D / 32) + half * NB;
-            const uint16_t * vn = a.v_norms + row * (D / 32) + half * NB;
-            const uint32_t nd = dst + (uint32_t)(kTile * 4 * C::CHUNK + r * C::NORMS);
-            copy_or_zero<C::NORMS>(nd, what == 0 ? kn : vn, live);
-            if (what == 0) copy_or_zero<C::NORMS>(nd + (uint32_t)(kTile * C::NORMS), vn, live);
+                if (i < bits) copy_or_zero<C::CHUNK>(dst + (uint32_t)((i * 2 * kTile + u) * C::CHUNK), c + i * C::NBT, live);
+            // the word that holds the norms of these blocks
+            const int64_t at = row * (D / 32) + half * NB + (NB == 4 ? 2 * side : 0);
+            const uint32_t nd = dst + (uint32_t)(2 * kTile * 4 * C::CHUNK + 4 * u);
+            copy_or_zero<4>(nd, (what == 0 ? a.k_norms : a.v_norms) + at, live);
+            if (what == 0) copy_or_zero<4>(nd + (uint32_t)(8 * kTile), a.v_norms + at, live);
         };
         auto advance = [&] {
             if (++half < NH) return;
@@ -694,53 +782,43 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
         }
         while (left > 0) {
             const int s = ring % ST;
-            const bool ok = ring < ST || (tc::mbar_wait(empty + 8u * s, (uint32_t)((ring / ST - 1) & 1), fm::kWaitNs) && *s_err == 0);
+            const bool ok = ring < ST || fm::wait(empty + 8u * s, (uint32_t)((ring / ST - 1) & 1));
             if (!__all_sync(0xffffffffu, ok)) {
                 *s_err = 1;
                 break;
             }
             asm volatile("cp.async.wait_group 2;" ::: "memory");
             const unsigned char * src = smem + C::OFF_PACKED + slot * C::PACKED;
-            uint32_t w[4 * NB], norm[NB / 2], other[NB / 2];
+            uint32_t w[4 * C::NBT];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if constexpr (NB == 4) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(src + (i * kTile + r) * 16);
-                    w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+                if constexpr (C::NBT == 2) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(src + (i * 2 * kTile + u) * 8);
+                    w[2 * i] = x.x; w[2 * i + 1] = x.y;
                 } else {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(src + (i * kTile + r) * 8);
-                    w[2 * i] = u.x; w[2 * i + 1] = u.y;
+                    w[i] = *reinterpret_cast<const uint32_t *>(src + (i * 2 * kTile + u) * 4);
                 }
             }
-#pragma unroll
-            for (int i = 0; i < NB / 2; ++i) {
-                const uint32_t * n = reinterpret_cast<const uint32_t *>(src + kTile * 4 * C::CHUNK + r * C::NORMS) + i;
-                norm[i] = n[0];
-                other[i] = n[kTile * NB / 2];
-            }
+            const uint32_t * nw = reinterpret_cast<const uint32_t *>(src + 2 * kTile * 4 * C::CHUNK) + u;
+            uint32_t norm = nw[0];
+            const uint32_t other = nw[2 * kTile];
             const int item = flags[0];
             flags[0] = flags[1];
             flags[1] = flags[2];
             --left;
             // a key with an infinite or NaN norm marks its readers' sums, and takes
             // no part in the products
-            uint32_t bad = 0u;
-#pragma unroll
-            for (int i = 0; i < NB / 2; ++i)
-                bad |= ((norm[i] & 0x7C007C00u) + 0x04000400u) | (item & 1 ? 0u : (other[i] & 0x7C007C00u) + 0x04000400u);
-            bad &= 0x80008000u;
+            const uint32_t bad = (((norm & 0x7C007C00u) + 0x04000400u) | (item & 1 ? 0u : (other & 0x7C007C00u) + 0x04000400u)) & 0x80008000u;
             if ((item & 1) == 0) {
                 const uint32_t keys = __ballot_sync(0xffffffffu, bad != 0u);
                 if (lane == 0) {
-                    volatile uint32_t * word = s_bad + 4 * (tile & 7) + (warp - 4 * WGS);
+                    volatile uint32_t * word = s_bad + 8 * (tile & 7) + (warp - 4 * WGS);
                     *word = item == 0 ? keys : *word | keys;
                 }
                 if (NH == 1 || item != 0) ++tile;
             }
-            if (bad != 0u) {
-#pragma unroll
-                for (int i = 0; i < NB / 2; ++i) norm[i] = 0u;
-            }
+            if (bad != 0u) norm = 0u;
+            if (NB == 2) norm = side ? norm >> 16 : norm;
             if (more) {
                 fetch(slot);
                 flags[2] = what | half << 1;
@@ -754,9 +832,9 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
             uint32_t tab[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) tab[i] = item & 1 ? a.v_table[i] : a.k_table[i];
-            if (bits == 4) unpack_row<4, NB>(w, norm, tab, dst, r & 7);
-            else if (bits == 3) unpack_row<3, NB>(w, norm, tab, dst, r & 7);
-            else unpack_row<2, NB>(w, norm, tab, dst, r & 7);
+            if (bits == 4) unpack_row<4, C::NBT>(w, norm, tab, dst, side, r & 7);
+            else if (bits == 3) unpack_row<3, C::NBT>(w, norm, tab, dst, side, r & 7);
+            else unpack_row<2, C::NBT>(w, norm, tab, dst, side, r & 7);
             tc::fence_proxy_async();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(full + 8u * s);
@@ -772,7 +850,7 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
         const uint32_t o_tm = lane_tm + fm::kOutCol + (uint32_t)(w * D);
         bool ok = true;
         int tile0 = 0;                       // key tiles of the parts before
-        int mine = 0;                        // tiles that this warpgroup has done
+        int mine = 0, done = 0;              // tiles and parts that this warpgroup has done
         while (ok && it.next(a, p)) {
             const int in_set = MODE == PAIR ? w * kTile + r : r;       // row of the set
             const bool valid = in_set < p.rows;
@@ -795,43 +873,52 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
             const bool warp_valid = (MODE == PAIR ? w * kTile : 0) + (r & ~31) < p.rows;
             fm::RowState st{-CUDART_INF_F, 0.0f};
             bool first = true;
-            for (int j = MODE == STREAM ? w : 0; j < p.tiles; j += MODE == STREAM ? 2 : 1) {
+            for (int j = MODE == STREAM ? w : 0; j < p.tiles && ok; j += MODE == STREAM ? 2 : 1) {
                 const int slot = MODE == WIDE ? (tile0 + j) & 1 : w;
-                const int use = MODE == WIDE ? (tile0 + j) >> 1 : mine;
-                ok = tc::mbar_wait(s_full + 8u * slot, (uint32_t)(use & 1), fm::kWaitNs) && *s_err == 0;
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc::fence_after_sync();
-                if (warp_valid) {
-                    const uint32_t s_tm = lane_tm + (uint32_t)slot * fm::kSlotCols;
-                    auto wait_acc = [&] { return tc::mbar_wait(o_done + 8u * w, (uint32_t)((mine - 1) & 1), fm::kWaitNs); };
-                    const int t0 = (p.tile0 + j) * kTile;
-                    uint32_t allowed[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-                    if (t0 + kTile > ctx0) {
+                const uint32_t use = MODE == WIDE ? (uint32_t)(tile0 + j) >> 1 : (uint32_t)mine;
+                const int t0 = (p.tile0 + j) * kTile;
+                const bool edge = t0 + kTile > ctx0;
+                uint32_t allowed[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+                if (edge && warp_valid) {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int c = p.rq.len - (t0 + 32 * x);    // tokens left
-                            const uint32_t in = c >= 32 ? 0xFFFFFFFFu : c <= 0 ? 0u : (1u << c) - 1u;
-                            allowed[x] = valid ? in & (in != 0u ? mask32(a, words, node, t0 + 32 * x - ctx0) : 0u) : 0u;
-                        }
-                        ok = fm::softmax_tile<false, true>(s_tm, o_tm, D, first, mul, allowed, st, wait_acc);
-                    } else {
-                        ok = fm::softmax_tile<false, false>(s_tm, o_tm, D, first, mul, nullptr, st, wait_acc);
+                    for (int x = 0; x < 4; ++x) {
+                        const int c = p.rq.len - (t0 + 32 * x);    // tokens left
+                        const uint32_t in = c >= 32 ? 0xFFFFFFFFu : c <= 0 ? 0u : (1u << c) - 1u;
+                        allowed[x] = valid ? in & (in != 0u ? mask32(a, words, node, t0 + 32 * x - ctx0) : 0u) : 0u;
                     }
-                    const volatile uint32_t * bad = s_bad + 4 * ((tile0 + j) & 7);
-                    if (((bad[0] & allowed[0]) | (bad[1] & allowed[1]) | (bad[2] & allowed[2]) | (bad[3] & allowed[3])) != 0u)
-                        st.sum = CUDART_NAN_F;
+                }
+#pragma unroll 1
+                for (int g = 0; g < 2; ++g) {
+                    // (the scores that follow in this half wait for these weights)
+                    ok = fm::wait(s_full + 8u * (2 * slot + g), use & 1u);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    if (warp_valid) {
+                        // products so far: half 1 of the tile before -- its scores were behind
+                        // those of the tile in front, or WIDE two in front -- then, in this
+                        // half 1, those of half 0
+                        auto scale_acc = [&](float f) {
+                            bool r = first || fm::wait(o_done + 8u * (2 * w + 1), (uint32_t)((mine - 1) & 1));
+                            if (g == 1) r = r && fm::wait(o_done + 8u * (2 * w), (uint32_t)(mine & 1));
+                            fm::rescale(o_tm, D, f);
+                            return r;
+                        };
+                        const uint32_t half = lane_tm + (uint32_t)slot * fm::kSlotCols + (uint32_t)g * fm::kHalfCols;
+                        const uint32_t al[2] = {g == 0 ? allowed[0] : allowed[2], g == 0 ? allowed[1] : allowed[3]};
+                        if (edge) ok = fm::softmax_half<false, true>(half, first && g == 0, mul, al, st, scale_acc);
+                        else ok = fm::softmax_half<false, false>(half, first && g == 0, mul, nullptr, st, scale_acc);
+                        const volatile uint32_t * bad = s_bad + 8 * ((tile0 + j) & 7) + 2 * g;
+                        if ((((bad[0] | bad[4]) & al[0]) | ((bad[1] | bad[5]) & al[1])) != 0u) st.sum = CUDART_NAN_F;
+                    }
+                    tc::mbar_arrive(p_full + 8u * (2 * slot + g));
                 }
                 first = false;
                 ++mine;
-                tc::mbar_arrive(p_full + 8u * slot);
             }
             tile0 += p.tiles;
-            // the last product (WIDE: the scores of a tile come before the products
-            // of the one in front of it, so that one is waited for first: a wait
-            // may be one phase ahead of the barrier, not two)
-            if (MODE == WIDE && mine > 1) ok = ok && tc::mbar_wait(o_done, (uint32_t)(mine & 1), fm::kWaitNs);
-            ok = ok && tc::mbar_wait(o_done + 8u * w, (uint32_t)((mine - 1) & 1), fm::kWaitNs);
+            ok = ok && fm::wait(o_last + 8u * w, (uint32_t)(done & 1));
+            ++done;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc::fence_after_sync();
