@@ -108,6 +108,11 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
     return false;
 }
 
+// The same for a converged warp.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait(bar, parity));
+}
+
 // Position in a ring of N buffers: the buffer and the parity of its use.
 template <int N>
 struct Ring {
@@ -124,15 +129,50 @@ __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// D[tmem] (+)= A[tmem] B[smem], 16-bit A and B, fp32 D; A holds two values per
-// 32-bit column (16 of the contracted index in 8 columns).
-__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+// The issuing warps run converged, with one lane elected inside each
+// instruction: operands that are the same in all lanes then live in uniform
+// registers, which the MMAs read.  From a branch that one lane takes, every
+// operand is moved there first, MMA by MMA.
+__device__ __forceinline__ uint32_t elected() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(e));
+    return e;
+}
+
+// D[tmem] (+)= A[smem] B[smem] by the elected lane, 16-bit A and B, fp32 D.
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                        uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
-        :: "r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate));
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
+        :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead));
+}
+
+// The same with A in TMEM, two values per 32-bit column (16 of the contracted
+// index in 8 columns).
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+        :: "r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead));
+}
+
+// An arrival on `bar` when the MMAs that the elected lane issued are done.
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n"
+        :: "r"(bar), "r"(lead) : "memory");
 }
 
 // The same value; keeps the compiler from holding sums of it in registers

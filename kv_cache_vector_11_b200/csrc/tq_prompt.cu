@@ -132,7 +132,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
     unsigned char * smem = smem_raw + (sbase - raw);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t bar = sbase + (uint32_t)C::OFF_BAR;
     const uint32_t q_full = bar, full = bar + 8u, empty = full + 8u * ST, s_full = empty + 8u * ST,
                    p_full = s_full + 32u, o_done = p_full + 32u, o_last = o_done + 32u, s_free = o_last + 16u,
@@ -226,7 +226,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         __syncthreads();
         tc::fence_after_sync();
     }
-    const uint32_t tmem = n > 0 ? *s_tmem : 0u;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, n > 0 ? *s_tmem : 0u, 0);
     const int ctrl = warp - 4 * NQ;                       // 0 and 3: MMAs, 1: copies, 2: value scan
 
     if (n > 0 && ctrl == 1) {
@@ -269,8 +269,9 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         // as the tensor core works on it, a wait or a commit costs some 100 cycles
         // more; with two threads those of one overlap the products of the other
         // (8192-token prompt, d = 128: 0.579 ms with one thread, MMA2 with two). ----
-        const int t = ctrl == 0 ? 0 : 1;
-        if (lane == 0 && (NQ == 1 || t < slots)) {
+        const int t = ctrl == 0 ? 0 : 1;                  // (the same in all lanes)
+        if (NQ == 1 || t < slots) {
+            const uint32_t lead = fm::elected();
             constexpr uint32_t id_qk = fm::idesc(BF16, kTile, false), id_qk64 = fm::idesc(BF16, 64, false), id_pv = fm::idesc(BF16, C::W, true);
             const uint64_t kv_desc = tc::smem_desc_sw128(sbase + (uint32_t)C::OFF_KV);
             const uint64_t v_desc = fm::smem_desc_sw128_mn(sbase + (uint32_t)C::OFF_KV, (uint32_t)C::SLICE);
@@ -282,7 +283,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
 #pragma unroll
                 for (int ks = 0; ks < C::W / 16; ++ks) {
                     const uint64_t off = (uint64_t)(((ks >> 2) * C::SLICE + (ks & 3) * 32) >> 4);
-                    tc::mma_bf16(tmem + (uint32_t)s * fm::kSlotCols + (uint32_t)key, qd + off, kd + off, id, h > 0 || ks > 0 ? 1u : 0u);
+                    fm::mma_ss(lead, tmem + (uint32_t)s * fm::kSlotCols + (uint32_t)key, qd + off, kd + off, id, h > 0 || ks > 0 ? 1u : 0u);
                 }
             };
             // weights of half g of slot s times the columns h of the value tile in
@@ -291,23 +292,23 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                 const uint64_t vd = v_desc + (uint64_t)(b * (uint32_t)(C::BUF >> 4) + 512u * (uint32_t)g);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    fm::mma_ts(tmem + fm::kOutCol + (uint32_t)(i * D + h * C::W),
+                    fm::mma_ts(lead, tmem + fm::kOutCol + (uint32_t)(i * D + h * C::W),
                                tmem + (uint32_t)s * fm::kSlotCols + (uint32_t)g * fm::kHalfCols + 8u * k, vd + 128u * k, id_pv,
                                acc || k > 0 ? 1u : 0u);
             };
-            bool ok = fm::wait(q_full, 0u);
+            bool ok = fm::wait_warp(q_full, 0u);
             fm::Ring<ST> ring;                            // the next buffer
             if constexpr (NQ == 2) {
                 // thread t: row tile t.  The scores of a half come behind the
                 // products that read the weights they overwrite.
                 const uint32_t sf = s_full + 16u * t, pf = p_full + 16u * t, od = o_done + 16u * t;
-                ok = ok && fm::wait(full, 0u);
+                ok = ok && fm::wait_warp(full, 0u);
                 if (ok) {
                     for (int g = 0; g < 2; ++g) {
                         qk(t, t, 0, 0u, 64 * g, id_qk64);
-                        tc::commit(sf + 8u * g);
+                        fm::commit(lead, sf + 8u * g);
                     }
-                    tc::commit(empty);
+                    fm::commit(lead, empty);
                 }
                 ring.step();
                 for (int j = 0; j < n && ok; ++j) {
@@ -316,46 +317,46 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     const uint32_t k = ring.at, kp = ring.parity;
                     ring.step();
                     const bool more = j + 1 < n;
-                    ok = fm::wait(full + 8u * v, vp);
-                    if (j < n_edge) ok = ok && fm::wait(scanned, (uint32_t)(j & 1));
-                    if (more) ok = ok && fm::wait(full + 8u * k, kp);
-                    ok = ok && fm::wait(pf, (uint32_t)(j & 1));
+                    ok = fm::wait_warp(full + 8u * v, vp);
+                    if (j < n_edge) ok = ok && fm::wait_warp(scanned, (uint32_t)(j & 1));
+                    if (more) ok = ok && fm::wait_warp(full + 8u * k, kp);
+                    ok = ok && fm::wait_warp(pf, (uint32_t)(j & 1));
                     if (!ok) break;
                     tc::fence_after_sync();
                     pv(t, t, 0, v, 0, j > 0);
                     if (more) {
                         qk(t, t, 0, k, 0, id_qk64);
-                        tc::commit(sf);
+                        fm::commit(lead, sf);
                     }
-                    tc::commit(od);
-                    ok = fm::wait(pf + 8u, (uint32_t)(j & 1));
+                    fm::commit(lead, od);
+                    ok = fm::wait_warp(pf + 8u, (uint32_t)(j & 1));
                     if (!ok) break;
                     tc::fence_after_sync();
                     pv(t, t, 0, v, 1, true);
                     if (more) {
                         qk(t, t, 0, k, 64, id_qk64);
-                        tc::commit(sf + 8u);
-                        tc::commit(empty + 8u * k);
+                        fm::commit(lead, sf + 8u);
+                        fm::commit(lead, empty + 8u * k);
                     }
-                    tc::commit(od + 8u);
-                    tc::commit(empty + 8u * v);
+                    fm::commit(lead, od + 8u);
+                    fm::commit(lead, empty + 8u * v);
                 }
-                if (ok) tc::commit(o_last + 8u * t);
+                if (ok) fm::commit(lead, o_last + 8u * t);
             } else if (t == 0) {
                 // scores: slot j & 1 is free again behind the products of tile j - 2
                 for (int j = 0; j < n && ok; ++j) {
-                    if (j > 1) ok = fm::wait(s_free + 8u * (j & 1), (uint32_t)(((j >> 1) - 1) & 1));
+                    if (j > 1) ok = fm::wait_warp(s_free + 8u * (j & 1), (uint32_t)(((j >> 1) - 1) & 1));
 #pragma unroll
                     for (int h = 0; h < NH; ++h) {
-                        ok = ok && fm::wait(full + 8u * ring.at, ring.parity);
+                        ok = ok && fm::wait_warp(full + 8u * ring.at, ring.parity);
                         if (!ok) break;
                         tc::fence_after_sync();
                         qk(0, j & 1, h, ring.at, 0, id_qk);
-                        tc::commit(empty + 8u * ring.at);
+                        fm::commit(lead, empty + 8u * ring.at);
                         ring.step();
                     }
                     for (int h = 0; h < NH; ++h) ring.step();                 // (the values)
-                    for (int g = 0; g < 2 && ok; ++g) tc::commit(s_full + 8u * (2 * (j & 1) + g));
+                    for (int g = 0; g < 2 && ok; ++g) fm::commit(lead, s_full + 8u * (2 * (j & 1) + g));
                 }
             } else {
                 // products
@@ -365,31 +366,31 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
 #pragma unroll
                     for (int h = 0; h < NH; ++h) {
                         b[h] = ring.at;
-                        ok = ok && fm::wait(full + 8u * ring.at, ring.parity);
+                        ok = ok && fm::wait_warp(full + 8u * ring.at, ring.parity);
                         ring.step();
                     }
-                    if (j < n_edge) ok = ok && fm::wait(scanned, (uint32_t)(j & 1));
+                    if (j < n_edge) ok = ok && fm::wait_warp(scanned, (uint32_t)(j & 1));
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
-                        ok = ok && fm::wait(p_full + 8u * (2 * (j & 1) + g), (uint32_t)((j >> 1) & 1));
+                        ok = ok && fm::wait_warp(p_full + 8u * (2 * (j & 1) + g), (uint32_t)((j >> 1) & 1));
                         if (!ok) break;
                         tc::fence_after_sync();
 #pragma unroll
                         for (int h = 0; h < NH; ++h) {
                             pv(0, j & 1, h, b[h], g, j > 0 || g > 0);
-                            if (g == 1) tc::commit(empty + 8u * b[h]);
+                            if (g == 1) fm::commit(lead, empty + 8u * b[h]);
                         }
-                        tc::commit(o_done + 8u * g);
+                        fm::commit(lead, o_done + 8u * g);
                     }
-                    if (ok) tc::commit(s_free + 8u * (j & 1));
+                    if (ok) fm::commit(lead, s_free + 8u * (j & 1));
                 }
-                if (ok) tc::commit(o_last);
+                if (ok) fm::commit(lead, o_last);
             }
             if (!ok) {
                 // the MMAs in flight end before their columns are freed
                 *s_err = 1;
-                tc::commit(drained + 8u * t);
-                fm::wait(drained + 8u * t, 0u);
+                fm::commit(lead, drained + 8u * t);
+                fm::wait_warp(drained + 8u * t, 0u);
             }
         }
         __syncwarp();
