@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
     const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
     unsigned char * smem = smem_raw + (sbase - raw);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t full = sbase + (uint32_t)C::OFF_BAR, empty = full + 8u * ST, s_full = empty + 8u * ST,
                    p_full = s_full + 32u, o_done = p_full + 32u, o_last = o_done + 32u, o_free = o_last + 16u,
                    s_free = o_free + 16u, drained = s_free + 16u, q_full = drained + 16u, q_free = q_full + 8u;
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = *s_tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
     PartIter it;
     it.start(a, *s_first);
     Part p;
@@ -499,7 +499,8 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                 ok = fm::wait(q_full, (uint32_t)(part & 1));
             }
             if (!ok) *s_err = 1;
-        } else if (t < 2 && lane == 0) {
+        } else if (t < 2) {
+            const uint32_t lead = fm::elected();
             constexpr uint32_t id_qk = fm::idesc(false, kTile, false), id_qk64 = fm::idesc(false, 64, false),
                                id_pv = fm::idesc(false, C::W, true);
             const uint64_t ring_desc = tc::smem_desc_sw128(sbase + (uint32_t)C::OFF_RING);
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
 #pragma unroll
                 for (int ks = 0; ks < C::W / 16; ++ks) {
                     const uint64_t off = (uint64_t)(((ks >> 2) * C::SLICE + (ks & 3) * 32) >> 4);
-                    tc::mma_bf16(tmem + (uint32_t)s * fm::kSlotCols + (uint32_t)key, qd + off, kd + off, id, h > 0 || ks > 0 ? 1u : 0u);
+                    fm::mma_ss(lead, tmem + (uint32_t)s * fm::kSlotCols + (uint32_t)key, qd + off, kd + off, id, h > 0 || ks > 0 ? 1u : 0u);
                 }
             };
             // weights of half g of slot s times the columns h of the value tile in
@@ -521,7 +522,7 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                 const uint64_t vd = v_desc + (uint64_t)(b * (uint32_t)(C::BUF >> 4) + 512u * (uint32_t)g);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    fm::mma_ts(tmem + fm::kOutCol + (uint32_t)(w * D + h * C::W),
+                    fm::mma_ts(lead, tmem + fm::kOutCol + (uint32_t)(w * D + h * C::W),
                                tmem + (uint32_t)s * fm::kSlotCols + (uint32_t)g * fm::kHalfCols + 8u * k, vd + 128u * k, id_pv,
                                acc || k > 0 ? 1u : 0u);
             };
@@ -531,7 +532,7 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
             uint32_t sf = s_full + 16u * t, pf = p_full + 16u * t, od = o_done + 16u * t;
             for (int part = 0; ok && it.next(a, p); ++part) {
                 // (every part in turn, also one that this thread has no share in)
-                ok = fm::wait(q_full, (uint32_t)(part & 1));
+                ok = fm::wait_warp(q_full, (uint32_t)(part & 1));
                 if (!ok) break;
                 if constexpr (MODE != WIDE) {
                     // Slot t: PAIR row tile t against every key tile; STREAM the one row
@@ -546,13 +547,13 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                     if (!takes) {
                         if constexpr (MODE == PAIR) {
                             for (int x = 0; x < 2 * p.tiles && ok; ++x) {
-                                ok = fm::wait(full + 8u * ring.at, ring.parity);
-                                tc::mbar_arrive(empty + 8u * ring.at);
+                                ok = fm::wait_warp(full + 8u * ring.at, ring.parity);
+                                if (lane == 0) tc::mbar_arrive(empty + 8u * ring.at);
                                 ring.step();
                             }
                         }
                         ring = next;
-                        tc::mbar_arrive(q_free);
+                        if (lane == 0) tc::mbar_arrive(q_free);
                         continue;
                     }
                     if (MODE == STREAM && t == 1) ring.step();
@@ -560,18 +561,18 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                     if (MODE == PAIR) vr.step();
                     else
                         for (int x = 0; x < (t == 0 ? (p.tiles > 1 ? 2 : 1) : (p.tiles > 2 ? 3 : 2)); ++x) vr.step();
-                    ok = fm::wait(full + 8u * kr.at, kr.parity);
+                    ok = fm::wait_warp(full + 8u * kr.at, kr.parity);
                     if (!ok) break;
                     tc::fence_after_sync();
                     for (int g = 0; g < 2; ++g) {
                         qk(i, t, 0, kr.at, 64 * g, id_qk64);
-                        tc::commit(sf + 8u * g);
+                        fm::commit(lead, sf + 8u * g);
                     }
-                    tc::commit(empty + 8u * kr.at);
+                    fm::commit(lead, empty + 8u * kr.at);
                     bool first = true;
                     for (int j = MODE == STREAM ? t : 0; j < p.tiles; j += stride) {
                         const bool more = j + stride < p.tiles;
-                        if (!more) tc::commit(q_free);       // (behind the part's last scores)
+                        if (!more) fm::commit(lead, q_free);       // (behind the part's last scores)
                         // the next key tile and this value tile
                         if (MODE == PAIR) {
                             kr.step();
@@ -580,25 +581,25 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                             // K(j + 2) is 4 on from K(j), or 3 from K(0)
                             for (int x = 0; x < (j == 0 ? 3 : 4); ++x) kr.step();
                         }
-                        ok = fm::wait(full + 8u * vr.at, vr.parity);
-                        if (more) ok = ok && fm::wait(full + 8u * kr.at, kr.parity);
+                        ok = fm::wait_warp(full + 8u * vr.at, vr.parity);
+                        if (more) ok = ok && fm::wait_warp(full + 8u * kr.at, kr.parity);
                         // the accumulator of the part before has been read
-                        if (first && finished > 0) ok = ok && fm::wait(o_free + 8u * t, (finished - 1) & 1u);
+                        if (first && finished > 0) ok = ok && fm::wait_warp(o_free + 8u * t, (finished - 1) & 1u);
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
-                            ok = ok && fm::wait(pf + 8u * g, use & 1u);
+                            ok = ok && fm::wait_warp(pf + 8u * g, use & 1u);
                             if (!ok) break;
                             tc::fence_after_sync();
                             pv(t, t, 0, vr.at, g, !first || g > 0);
                             if (more) {
                                 qk(i, t, 0, kr.at, 64 * g, id_qk64);
-                                tc::commit(sf + 8u * g);
+                                fm::commit(lead, sf + 8u * g);
                             }
-                            tc::commit(od + 8u * g);
+                            fm::commit(lead, od + 8u * g);
                         }
                         if (!ok) break;
-                        tc::commit(empty + 8u * vr.at);
-                        if (more) tc::commit(empty + 8u * kr.at);
+                        fm::commit(lead, empty + 8u * vr.at);
+                        if (more) fm::commit(lead, empty + 8u * kr.at);
                         first = false;
                         ++use;
                         if (MODE == PAIR) {
@@ -611,7 +612,7 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                         }
                     }
                     if (!ok) break;
-                    tc::commit(o_last + 8u * t);
+                    fm::commit(lead, o_last + 8u * t);
                     ++finished;
                     ring = next;
                 } else {
@@ -621,23 +622,23 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                         // filled twice in front of this thread
                         for (int j = 0; j < p.tiles && ok; ++j, ++use) {
                             // slot use & 1 is free behind the products of two tiles before
-                            if (use > 1) ok = fm::wait(s_free + 8u * (use & 1u), ((use >> 1) - 1) & 1u);
+                            if (use > 1) ok = fm::wait_warp(s_free + 8u * (use & 1u), ((use >> 1) - 1) & 1u);
 #pragma unroll
                             for (int h = 0; h < NH; ++h) {
-                                ok = ok && fm::wait(full + 8u * ring.at, ring.parity);
+                                ok = ok && fm::wait_warp(full + 8u * ring.at, ring.parity);
                                 if (!ok) break;
                                 tc::fence_after_sync();
                                 qk(0, (int)(use & 1u), h, ring.at, 0, id_qk);
-                                tc::commit(empty + 8u * ring.at);
+                                fm::commit(lead, empty + 8u * ring.at);
                                 ring.step();
                             }
                             if (!ok) break;
-                            for (int g = 0; g < 2; ++g) tc::commit(s_full + 8u * (2 * (use & 1u) + g));
-                            if (j + 1 == p.tiles) tc::commit(q_free);
+                            for (int g = 0; g < 2; ++g) fm::commit(lead, s_full + 8u * (2 * (use & 1u) + g));
+                            if (j + 1 == p.tiles) fm::commit(lead, q_free);
                             // over V(j - 1); behind the last keys over V(j) too
                             for (int v = (j > 0) + (j + 1 == p.tiles); v > 0; --v)
                                 for (int h = 0; h < NH; ++h) {
-                                    ok = ok && fm::wait(full + 8u * ring.at, ring.parity);
+                                    ok = ok && fm::wait_warp(full + 8u * ring.at, ring.parity);
                                     ring.step();
                                 }
                         }
@@ -647,31 +648,31 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                             if (j + 1 < p.tiles)
                                 for (int h = 0; h < NH; ++h) ring.step();            // K(j + 1)
                             // (the weights are there, so the buffers in front of V(j) are filled)
-                            ok = fm::wait(p_full + 16u * (use & 1u), (use >> 1) & 1u);
+                            ok = fm::wait_warp(p_full + 16u * (use & 1u), (use >> 1) & 1u);
                             uint32_t b[NH];
 #pragma unroll
                             for (int h = 0; h < NH; ++h) {
                                 b[h] = ring.at;
-                                ok = ok && fm::wait(full + 8u * ring.at, ring.parity);
+                                ok = ok && fm::wait_warp(full + 8u * ring.at, ring.parity);
                                 ring.step();
                             }
-                            if (j == 0 && finished > 0) ok = ok && fm::wait(o_free, (finished - 1) & 1u);
+                            if (j == 0 && finished > 0) ok = ok && fm::wait_warp(o_free, (finished - 1) & 1u);
 #pragma unroll
                             for (int g = 0; g < 2; ++g) {
-                                if (g == 1) ok = ok && fm::wait(p_full + 16u * (use & 1u) + 8u, (use >> 1) & 1u);
+                                if (g == 1) ok = ok && fm::wait_warp(p_full + 16u * (use & 1u) + 8u, (use >> 1) & 1u);
                                 if (!ok) break;
                                 tc::fence_after_sync();
 #pragma unroll
                                 for (int h = 0; h < NH; ++h) {
                                     pv(0, (int)(use & 1u), h, b[h], g, j > 0 || g > 0);
-                                    if (g == 1) tc::commit(empty + 8u * b[h]);
+                                    if (g == 1) fm::commit(lead, empty + 8u * b[h]);
                                 }
-                                tc::commit(o_done + 8u * g);
+                                fm::commit(lead, o_done + 8u * g);
                             }
-                            if (ok) tc::commit(s_free + 8u * (use & 1u));
+                            if (ok) fm::commit(lead, s_free + 8u * (use & 1u));
                         }
                         if (!ok) break;
-                        tc::commit(o_last);
+                        fm::commit(lead, o_last);
                         ++finished;
                     }
                 }
@@ -679,8 +680,8 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
             if (!ok) {
                 // the MMAs in flight end before their columns are freed
                 *s_err = 1;
-                tc::commit(drained + 8u * t);
-                fm::wait(drained + 8u * t, 0u);
+                fm::commit(lead, drained + 8u * t);
+                fm::wait_warp(drained + 8u * t, 0u);
             }
         }
         __syncwarp();
