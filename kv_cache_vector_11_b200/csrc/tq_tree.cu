@@ -52,7 +52,6 @@ namespace {
 using fm::kTile;
 
 constexpr int kTaMaxNodes = 256;
-constexpr int kTaAhead = 4;          // key tiles fetched into L2 ahead of their unpacking
 
 enum TreeMode { PAIR = 0, STREAM = 1, WIDE = 2 };
 
@@ -341,9 +340,11 @@ __device__ __forceinline__ void unpack_row(const uint32_t * w, uint32_t norms, c
                 // 24 bits -> 8 nibbles
                 const int bit = 24 * k, wi = 3 * blk + (bit >> 5), sh = bit & 31;
                 x = sh + 24 <= 32 ? w[wi] >> sh : __funnelshift_r(w[wi], w[wi + 1 < 3 * blk + 3 ? wi + 1 : wi], sh);
-                x = (x & 0x00000FFFu) | ((x << 4) & 0x0FFF0000u);
-                x = (x & 0x003F003Fu) | ((x << 2) & 0x3F003F00u);
-                x = (x & 0x07070707u) | ((x << 1) & 0x70707070u);
+                // (a step keeps the lower part and takes the rest from the shifted
+                // word; what it takes too much the last step drops)
+                x = (x & 0x00000FFFu) | ((x * 16u) & ~0x00000FFFu);
+                x = (x & 0x003F003Fu) | ((x * 4u) & ~0x003F003Fu);
+                x = (x & 0x07070707u) | ((x * 2u) & 0x70707070u);
             } else {
                 // 16 bits -> 8 nibbles
                 x = (w[2 * blk + (k >> 1)] >> (16 * (k & 1))) & 0xFFFFu;
@@ -695,57 +696,53 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
         // key tile j and the value tile j - LEAD
         int step = 0, half = 0, what = 0;
         bool more = it.next(a, p);
-        // Tile `tile` into L2, 16 rows by every 16th thread; the page was read
-        // a step earlier, so that nothing waits for it here.
-        int ahead = 0;
-        auto read_ahead = [&](int tile) {
-            const int t0 = tile * kTile + r;
-            ahead = t0 < p.rq.len ? __ldg(a.table + (int64_t)p.b * a.max_pages + (t0 >> a.page_shift)) : 0;
+        // Cache row of this thread's token in key tile `tile` of the part, kNone
+        // past the last token.  (32 bits: the host refuses larger storage.)
+        constexpr uint32_t kNone = 0xFFFFFFFFu;
+        auto page_of = [&](int t) { return __ldg(a.table + (int64_t)p.b * a.max_pages + (t >> a.page_shift)); };
+        auto row_of = [&](int page, int t) {
+            const uint32_t pg = (uint32_t)min(max(page, 0), a.n_pages - 1);
+            return ((pg * (uint32_t)a.n_kv_heads + (uint32_t)p.hk) << a.page_shift) + ((uint32_t)t & ((1u << a.page_shift) - 1u));
         };
-        auto fetch_ahead = [&](int tile) {
-            const int t0 = tile * kTile + r;
-            if ((u & 15) != 0 || u >= kTile || t0 >= p.rq.len) return;
-            const int pg = min(max(ahead, 0), a.n_pages - 1);
-            const int64_t row = (((int64_t)pg * a.n_kv_heads + p.hk) << a.page_shift) + (t0 & ((1 << a.page_shift) - 1));
-            auto pre = [](const void * ptr, uint32_t bytes) {
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(ptr), "r"(bytes) : "memory");
-            };
-            pre(a.k_codes + row * (D / 32 * a.k_bits), (uint32_t)(16 * D / 8 * a.k_bits));
-            pre(a.v_codes + row * (D / 32 * a.v_bits), (uint32_t)(16 * D / 8 * a.v_bits));
-            pre(a.k_norms + row * (D / 32), (uint32_t)(16 * D / 16));
-            pre(a.v_norms + row * (D / 32), (uint32_t)(16 * D / 16));
+        // (its page was read a step earlier: the read takes as long as half a step)
+        int page = 0;
+        auto read_page = [&](int tile) {
+            const int t = (p.tile0 + tile) * kTile + r;
+            if (tile < p.tiles && t < p.rq.len) page = page_of(t);
         };
-        auto start_ahead = [&] {
-            for (int j = 1; j <= kTaAhead + 1; ++j) {
-                if (j < p.tiles) read_ahead(p.tile0 + j);
-                if (j < p.tiles && j <= kTaAhead) fetch_ahead(p.tile0 + j);
-            }
+        auto tile_row = [&](int tile) {
+            const int t = (p.tile0 + tile) * kTile + r;
+            return t < p.rq.len ? row_of(page, t) : kNone;
         };
-        // The packed words and norms of this thread's row of the item at (step,
-        // what, half), into slot `slot`; every thread reads back only what it
-        // copied itself.
+        uint32_t row_k = kNone, row_v = kNone;           // rows of the key and the value tile of this step
+        auto start_part = [&] {
+            read_page(0);
+            row_k = tile_row(0);
+            if (LEAD == 0) row_v = row_k;
+            read_page(1);
+        };
+        // The packed words and norms of this thread's side of a row, into slot
+        // `slot`; every thread reads back only what it copied itself.
         const uint32_t packed = sbase + (uint32_t)C::OFF_PACKED;
         auto fetch = [&](int slot) {
-            const int j = what == 0 ? step : step - LEAD;
-            const int t = (p.tile0 + j) * kTile + r;
-            const bool live = t < p.rq.len;
+            const uint32_t row = what == 0 ? row_k : row_v;
+            const bool live = row != kNone;
+            const uint64_t at = live ? row : 0u;
             const int bits = what == 0 ? a.k_bits : a.v_bits;
-            int pg = 0;
-            if (live) pg = min(max(__ldg(a.table + (int64_t)p.b * a.max_pages + (t >> a.page_shift)), 0), a.n_pages - 1);
-            const int64_t row = live ? (((int64_t)pg * a.n_kv_heads + p.hk) << a.page_shift) + (t & ((1 << a.page_shift) - 1)) : 0;
-            const uint32_t * c = (what == 0 ? a.k_codes : a.v_codes) + row * (D / 32 * bits) + half * (NB * bits) + side * (C::NBT * bits);
+            const uint32_t * c = (what == 0 ? a.k_codes : a.v_codes) + at * (uint32_t)(D / 32 * bits) +
+                                 (uint32_t)((NH == 1 ? side : 2 * half + side) * C::NBT * bits);
             const uint32_t dst = packed + (uint32_t)(slot * C::PACKED);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (i < bits) copy_or_zero<C::CHUNK>(dst + (uint32_t)((i * 2 * kTile + u) * C::CHUNK), c + i * C::NBT, live);
             // the word that holds the norms of these blocks
-            const int64_t at = row * (D / 32) + half * NB + (NB == 4 ? 2 * side : 0);
+            const uint64_t nat = at * (D / 32) + (uint32_t)(half * NB + (NB == 4 ? 2 * side : 0));
             const uint32_t nd = dst + (uint32_t)(2 * kTile * 4 * C::CHUNK + 4 * u);
-            copy_or_zero<4>(nd, (what == 0 ? a.k_norms : a.v_norms) + at, live);
-            if (what == 0) copy_or_zero<4>(nd + (uint32_t)(8 * kTile), a.v_norms + at, live);
+            copy_or_zero<4>(nd, (what == 0 ? a.k_norms : a.v_norms) + nat, live);
+            if (what == 0) copy_or_zero<4>(nd + (uint32_t)(8 * kTile), a.v_norms + nat, live);
         };
         auto advance = [&] {
-            if (++half < NH) return;
+            if (NH == 2 && ++half < NH) return;
             half = 0;
             // after the keys of this step its values, if any; then the next step
             if (what == 0 && step >= LEAD) {
@@ -753,9 +750,12 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                 return;
             }
             what = 0;
-            if (++step < p.tiles) {
-                if (step + kTaAhead < p.tiles) fetch_ahead(p.tile0 + step + kTaAhead);
-                if (step + kTaAhead + 1 < p.tiles) read_ahead(p.tile0 + step + kTaAhead + 1);
+            ++step;
+            if (LEAD == 1) row_v = row_k;
+            if (step < p.tiles) {
+                row_k = tile_row(step);
+                read_page(step + 1);
+                if (LEAD == 0) row_v = row_k;
                 return;
             }
             if (step < p.tiles + LEAD) {
@@ -764,16 +764,17 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
             }
             step = 0;
             more = it.next(a, p);
-            if (more) start_ahead();
+            if (more) start_part();
         };
         // Three items are on their way while one is unpacked; flags: bit 0 values,
         // bit 1 second half.
-        int ring = 0, tile = 0, slot = 0, flags[3], left = 0;
+        fm::Ring<ST> ring;
+        int filled = 0, tile = 0, slot = 0, flags[3], left = 0;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             flags[k] = 0;
             if (more) {
-                if (k == 0) start_ahead();
+                if (k == 0) start_part();
                 fetch(k);
                 flags[k] = what | half << 1;
                 ++left;
@@ -782,8 +783,8 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
         while (left > 0) {
-            const int s = ring % ST;
-            const bool ok = ring < ST || fm::wait(empty + 8u * s, (uint32_t)((ring / ST - 1) & 1));
+            const uint32_t s = ring.at;
+            const bool ok = filled < ST || fm::wait(empty + 8u * s, ring.parity ^ 1u);
             if (!__all_sync(0xffffffffu, ok)) {
                 *s_err = 1;
                 break;
@@ -839,7 +840,8 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
             tc::fence_proxy_async();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(full + 8u * s);
-            ++ring;
+            ring.step();
+            if (filled < ST) ++filled;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else {
@@ -1134,6 +1136,8 @@ extern "C" tq_status tq_tree_attention(const tq_rotation * rot, int32_t k_bits, 
     if (n_pages < 1 || max_pages < 1) return fail(TQ_ERR_INVALID_ARG, "n_pages and max_pages must be >= 1");
     if (max_len > (int64_t)max_pages * page_size)
         return fail(TQ_ERR_INVALID_ARG, "max_len exceeds max_pages * page_size");
+    if ((int64_t)n_pages * n_kv_heads > (int64_t)(0xFFFFFFFFu / (uint32_t)page_size))
+        return fail(TQ_ERR_UNSUPPORTED, "2^32 cache rows or more");
     if (tree_mask && (mask_words < (max_nodes + 63) / 64))
         return fail(TQ_ERR_INVALID_ARG, "mask_words below ceil(max_nodes / 64)");
     if (std::isnan(scale) || std::isinf(scale)) return fail(TQ_ERR_INVALID_ARG, "scale is not finite");
