@@ -322,40 +322,50 @@ __device__ __forceinline__ uint4 lookup8(uint32_t x, const uint32_t * tab, __hal
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// One side of a row of an operand buffer: NB blocks of BITS words, their norms
-// in one word.
-template <int BITS, int NB>
-__device__ __forceinline__ void unpack_row(const uint32_t * w, uint32_t norms, const uint32_t * tab, unsigned char * dst,
-                                           int side, int swz) {
+// Block `blk` of a row of an operand buffer: BITS words (the first of w), the
+// norm twice.
+template <int BITS>
+__device__ __forceinline__ void unpack_block(const uint32_t * w, uint32_t nn, const uint32_t * tab, unsigned char * dst, int blk,
+                                             int swz) {
+    const __half2 norm = *reinterpret_cast<const __half2 *>(&nn);
+    dst += (blk >> 1) * (kTile * 128);
+    const int c0 = (4 * (blk & 1)) ^ swz;                // 16-byte chunk of the 128-byte row, swizzled
 #pragma unroll
-    for (int blk = 0; blk < NB; ++blk) {
-        const uint32_t nn = __byte_perm(norms, 0u, blk ? 0x3232 : 0x1010);
-        const __half2 norm = *reinterpret_cast<const __half2 *>(&nn);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t x;
-            if constexpr (BITS == 4) {
-                x = w[4 * blk + k];
-            } else if constexpr (BITS == 3) {
-                // 24 bits -> 8 nibbles
-                const int bit = 24 * k, wi = 3 * blk + (bit >> 5), sh = bit & 31;
-                x = sh + 24 <= 32 ? w[wi] >> sh : __funnelshift_r(w[wi], w[wi + 1 < 3 * blk + 3 ? wi + 1 : wi], sh);
-                // (a step keeps the lower part and takes the rest from the shifted
-                // word; what it takes too much the last step drops)
-                x = (x & 0x00000FFFu) | ((x * 16u) & ~0x00000FFFu);
-                x = (x & 0x003F003Fu) | ((x * 4u) & ~0x003F003Fu);
-                x = (x & 0x07070707u) | ((x * 2u) & 0x70707070u);
-            } else {
-                // 16 bits -> 8 nibbles
-                x = (w[2 * blk + (k >> 1)] >> (16 * (k & 1))) & 0xFFFFu;
-                x = (x | (x << 8)) & 0x00FF00FFu;
-                x = (x | (x << 4)) & 0x0F0F0F0Fu;
-                x = (x | (x << 2)) & 0x33333333u;
-            }
-            // 16-byte chunk of the row: two blocks of a side fill a slice, one block half of it
-            const int c = NB == 2 ? 4 * blk + k : 4 * side + k;
-            *reinterpret_cast<uint4 *>(dst + (NB == 2 ? side * (kTile * 128) : 0) + 16 * (c ^ swz)) = lookup8<BITS == 4>(x, tab, norm);
+    for (int k = 0; k < 4; ++k) {
+        uint32_t x;
+        if constexpr (BITS == 4) {
+            x = w[k];
+        } else if constexpr (BITS == 3) {
+            // 24 bits -> 8 nibbles (a step keeps the lower part and takes the rest
+            // from the shifted word; what it takes too much the last step drops)
+            const int wi = 24 * k / 32, sh = 24 * k % 32;
+            x = sh + 24 <= 32 ? w[wi] >> sh : __funnelshift_r(w[wi], w[wi < 2 ? wi + 1 : 2], sh);
+            x = (x & 0x00000FFFu) | ((x * 16u) & ~0x00000FFFu);
+            x = (x & 0x003F003Fu) | ((x * 4u) & ~0x003F003Fu);
+            x = (x & 0x07070707u) | ((x * 2u) & 0x70707070u);
+        } else {
+            // 16 bits -> 8 nibbles
+            x = (w[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
+            x = (x | (x * 256u)) & 0x00FF00FFu;
+            x = (x | (x * 16u)) & 0x0F0F0F0Fu;
+            x = (x | (x * 4u)) & 0x33333333u;
         }
+        *reinterpret_cast<uint4 *>(dst + 16 * (c0 ^ k)) = lookup8<BITS == 4>(x, tab, norm);
+    }
+}
+
+// A row: NB blocks, one at a time (unrolled, the three widths are 30 KB of
+// instructions, more than stay close to the schedulers).
+template <int BITS, int NB>
+__device__ __forceinline__ void unpack_row(uint32_t * w, const uint32_t * norms, const uint32_t * tab, unsigned char * dst, int swz) {
+    uint64_t n = norms[0];
+    if constexpr (NB == 4) n |= (uint64_t)norms[1] << 32;
+#pragma unroll 1
+    for (int blk = 0; blk < NB; ++blk) {
+        unpack_block<BITS>(w, __byte_perm((uint32_t)n, 0u, 0x1010), tab, dst, blk, swz);
+        n >>= 16;
+#pragma unroll
+        for (int i = 0; i + BITS < BITS * NB; ++i) w[i] = w[i + BITS];
     }
 }
 
@@ -390,22 +400,23 @@ struct TaCfg {
     static constexpr int SLICE = kTile * 128;            // 64 columns of 128 rows
     static constexpr int BUF = W / 64 * SLICE;
     static constexpr int QT = MODE == PAIR ? 2 : 1;      // row tiles
-    static constexpr int LEAD = MODE == PAIR ? 0 : 1;    // tiles that the keys are ahead of the values
+    // one ring of key buffers and one of value buffers; STREAM: three of values,
+    // so that a thread that takes every other tile sees each buffer's uses in order
     static constexpr int OFF_RING = QT * NH * BUF;
-    static constexpr int STAGES = (192 * 1024 - OFF_RING) / BUF < 8 ? (192 * 1024 - OFF_RING) / BUF : 8;
-    static constexpr int THREADS = 128 * (WGS + 3);      // softmax, two warpgroups of unpacking, the issuing threads
-    // packed rows on their way, two threads a row: codes as 4 chunks x 256
-    // threads x CHUNK bytes, then one word of norms and one of the other norms
-    static constexpr int NBT = NB / 2;                   // blocks of a thread
-    static constexpr int CHUNK = 4 * NBT;
+    static constexpr int NK = D == 64 ? 4 : 2, NV = D == 64 ? 4 : MODE == STREAM ? 3 : 2;
+    static constexpr int STAGES = NK + NV;
+    static constexpr int THREADS = 128 * (WGS + 3);      // softmax, unpacking keys and values, the issuing threads
+    // packed rows on their way, one thread a row: codes as 4 chunks x 128 threads
+    // x CHUNK bytes, the norms, and (keys) the norms of the values
+    static constexpr int CHUNK = 4 * NB, NORMS = 2 * NB;
     static constexpr int OFF_PACKED = OFF_RING + STAGES * BUF;
-    static constexpr int PACKED = 2 * kTile * (4 * CHUNK + 8);
+    static constexpr int PACKED = kTile * (4 * CHUNK + 2 * NORMS);
     // mbarriers: full[STAGES], empty[STAGES], s_full[2][2], p_full[2][2],
     // o_done[2][2], o_last[2], o_free[2], s_free[2], drained[2], q_full, q_free
-    static constexpr int OFF_BAR = OFF_PACKED + 3 * PACKED;
+    static constexpr int OFF_BAR = OFF_PACKED + 2 * PACKED;
     static constexpr int N_BAR = 2 * STAGES + 22;
-    static constexpr int OFF_BAD = (OFF_BAR + 8 * N_BAR + 15) / 16 * 16;    // 8 tiles x two threads a row x 128 bits: keys with a bad norm
-    static constexpr int OFF_MISC = OFF_BAD + 256;                           // TMEM address, error flag, first request
+    static constexpr int OFF_BAD = (OFF_BAR + 8 * N_BAR + 15) / 16 * 16;    // 8 tiles x 128 bits: keys with a bad norm
+    static constexpr int OFF_MISC = OFF_BAD + 128;                           // TMEM address, error flag, first request
     static constexpr int SMEM = OFF_MISC + 16 + 1024;                       // + alignment of the base
     static_assert(SMEM <= 232448, "shared memory of a CTA");
     // registers a thread: 96 at launch (640 threads) or 128 (512)
@@ -430,7 +441,7 @@ template <int D, int MODE>
 __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const __grid_constant__ TreeArgs a,
                                                                            const __grid_constant__ CUtensorMap qmap) {
     using C = TaCfg<D, MODE>;
-    constexpr int WGS = C::WGS, NH = C::NH, NB = C::NB, ST = C::STAGES, LEAD = C::LEAD;
+    constexpr int WGS = C::WGS, NH = C::NH, NB = C::NB, ST = C::STAGES;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -446,7 +457,7 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
 
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
-            tc::mbar_init(full + 8u * i, 8);
+            tc::mbar_init(full + 8u * i, 4);
             tc::mbar_init(empty + 8u * i, MODE == PAIR ? 2 : 1);
         }
         for (int i = 0; i < 4; ++i) {
@@ -527,10 +538,12 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                                tmem + (uint32_t)s * fm::kSlotCols + (uint32_t)g * fm::kHalfCols + 8u * k, vd + 128u * k, id_pv,
                                acc || k > 0 ? 1u : 0u);
             };
-            fm::Ring<ST> ring;                               // the next buffer
+            fm::Ring<C::NK> kr;                              // the next key and value buffer
+            fm::Ring<C::NV> vr;
+            const uint32_t v_full = full + 8u * C::NK, v_empty = empty + 8u * C::NK;
             bool ok = true;
             uint32_t use = 0, finished = 0;                  // key tiles and parts of this thread so far
-            uint32_t sf = s_full + 16u * t, pf = p_full + 16u * t, od = o_done + 16u * t;
+            const uint32_t sf = s_full + 16u * t, pf = p_full + 16u * t, od = o_done + 16u * t;
             for (int part = 0; ok && it.next(a, p); ++part) {
                 // (every part in turn, also one that this thread has no share in)
                 ok = fm::wait_warp(q_full, (uint32_t)(part & 1));
@@ -538,30 +551,28 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                 if constexpr (MODE != WIDE) {
                     // Slot t: PAIR row tile t against every key tile; STREAM the one row
                     // tile against the key tiles t, t + 2, ...; the buffers between are
-                    // the other thread's.  No buffer is filled twice in front of a
-                    // thread that skips some: the ring is longer than what it skips.
+                    // the other thread's, and filled in order, so that the buffer waited
+                    // for is at its use or the one before.
                     const bool takes = MODE == PAIR ? t * kTile < p.rows : t < p.tiles;
                     const int i = MODE == PAIR ? t : 0, stride = MODE == PAIR ? 1 : 2;
-                    // ring positions: PAIR K0 V0 K1 V1 ..; STREAM K0 K1 V0 K2 V1 ..
-                    fm::Ring<ST> next = ring;
-                    for (int x = 0; x < 2 * p.tiles % (2 * ST); ++x) next.step();     // (whole turns change nothing)
                     if (!takes) {
-                        if constexpr (MODE == PAIR) {
-                            for (int x = 0; x < 2 * p.tiles && ok; ++x) {
-                                ok = fm::wait_warp(full + 8u * ring.at, ring.parity);
-                                if (lane == 0) tc::mbar_arrive(empty + 8u * ring.at);
-                                ring.step();
+                        for (int j = 0; j < p.tiles && ok; ++j) {
+                            if constexpr (MODE == PAIR) {
+                                ok = fm::wait_warp(full + 8u * kr.at, kr.parity);
+                                if (lane == 0) tc::mbar_arrive(empty + 8u * kr.at);
+                                ok = ok && fm::wait_warp(v_full + 8u * vr.at, vr.parity);
+                                if (lane == 0) tc::mbar_arrive(v_empty + 8u * vr.at);
                             }
+                            kr.step();
+                            vr.step();
                         }
-                        ring = next;
                         if (lane == 0) tc::mbar_arrive(q_free);
                         continue;
                     }
-                    if (MODE == STREAM && t == 1) ring.step();
-                    fm::Ring<ST> kr = ring, vr = ring;
-                    if (MODE == PAIR) vr.step();
-                    else
-                        for (int x = 0; x < (t == 0 ? (p.tiles > 1 ? 2 : 1) : (p.tiles > 2 ? 3 : 2)); ++x) vr.step();
+                    if (MODE == STREAM && t == 1) {
+                        kr.step();
+                        vr.step();
+                    }
                     ok = fm::wait_warp(full + 8u * kr.at, kr.parity);
                     if (!ok) break;
                     tc::fence_after_sync();
@@ -571,18 +582,13 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                     }
                     fm::commit(lead, empty + 8u * kr.at);
                     bool first = true;
-                    for (int j = MODE == STREAM ? t : 0; j < p.tiles; j += stride) {
+                    int j = MODE == STREAM ? t : 0;
+                    for (; j < p.tiles; j += stride) {
                         const bool more = j + stride < p.tiles;
-                        if (!more) fm::commit(lead, q_free);       // (behind the part's last scores)
-                        // the next key tile and this value tile
-                        if (MODE == PAIR) {
-                            kr.step();
-                            kr.step();
-                        } else {
-                            // K(j + 2) is 4 on from K(j), or 3 from K(0)
-                            for (int x = 0; x < (j == 0 ? 3 : 4); ++x) kr.step();
-                        }
-                        ok = fm::wait_warp(full + 8u * vr.at, vr.parity);
+                        if (!more) fm::commit(lead, q_free);     // (behind the part's last scores)
+                        kr.step();                               // to key tile j + stride
+                        if (MODE == STREAM && j + 1 < p.tiles) kr.step();
+                        ok = fm::wait_warp(v_full + 8u * vr.at, vr.parity);
                         if (more) ok = ok && fm::wait_warp(full + 8u * kr.at, kr.parity);
                         // the accumulator of the part before has been read
                         if (first && finished > 0) ok = ok && fm::wait_warp(o_free + 8u * t, (finished - 1) & 1u);
@@ -591,7 +597,7 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                             ok = ok && fm::wait_warp(pf + 8u * g, use & 1u);
                             if (!ok) break;
                             tc::fence_after_sync();
-                            pv(t, t, 0, vr.at, g, !first || g > 0);
+                            pv(t, t, 0, C::NK + vr.at, g, !first || g > 0);
                             if (more) {
                                 qk(i, t, 0, kr.at, 64 * g, id_qk64);
                                 fm::commit(lead, sf + 8u * g);
@@ -599,83 +605,60 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                             fm::commit(lead, od + 8u * g);
                         }
                         if (!ok) break;
-                        fm::commit(lead, empty + 8u * vr.at);
+                        fm::commit(lead, v_empty + 8u * vr.at);
                         if (more) fm::commit(lead, empty + 8u * kr.at);
+                        vr.step();
+                        if (MODE == STREAM && j + 1 < p.tiles) vr.step();
                         first = false;
                         ++use;
-                        if (MODE == PAIR) {
-                            vr.step();
-                            vr.step();
-                        } else {
-                            // V(j + 2) is 4 on from V(j); the last value tile is right
-                            // behind the one before it
-                            for (int x = 0; x < (j + 3 == p.tiles ? 3 : 4); ++x) vr.step();
-                        }
                     }
                     if (!ok) break;
                     fm::commit(lead, o_last + 8u * t);
                     ++finished;
-                    ring = next;
-                } else {
-                    // ring positions: K0 K1 V0 K2 V1 .., two buffers each
-                    if (t == 0) {
-                        // the last value tile of the part before is in: no buffer is then
-                        // filled twice in front of this thread
-                        for (int j = 0; j < p.tiles && ok; ++j, ++use) {
-                            // slot use & 1 is free behind the products of two tiles before
-                            if (use > 1) ok = fm::wait_warp(s_free + 8u * (use & 1u), ((use >> 1) - 1) & 1u);
+                } else if (t == 0) {
+                    for (int j = 0; j < p.tiles && ok; ++j, ++use) {
+                        // slot use & 1 is free behind the products of two tiles before
+                        if (use > 1) ok = fm::wait_warp(s_free + 8u * (use & 1u), ((use >> 1) - 1) & 1u);
 #pragma unroll
-                            for (int h = 0; h < NH; ++h) {
-                                ok = ok && fm::wait_warp(full + 8u * ring.at, ring.parity);
-                                if (!ok) break;
-                                tc::fence_after_sync();
-                                qk(0, (int)(use & 1u), h, ring.at, 0, id_qk);
-                                fm::commit(lead, empty + 8u * ring.at);
-                                ring.step();
-                            }
+                        for (int h = 0; h < NH; ++h) {
+                            ok = ok && fm::wait_warp(full + 8u * kr.at, kr.parity);
                             if (!ok) break;
-                            for (int g = 0; g < 2; ++g) fm::commit(lead, s_full + 8u * (2 * (use & 1u) + g));
-                            if (j + 1 == p.tiles) fm::commit(lead, q_free);
-                            // over V(j - 1); behind the last keys over V(j) too
-                            for (int v = (j > 0) + (j + 1 == p.tiles); v > 0; --v)
-                                for (int h = 0; h < NH; ++h) {
-                                    ok = ok && fm::wait_warp(full + 8u * ring.at, ring.parity);
-                                    ring.step();
-                                }
-                        }
-                    } else {
-                        for (int h = 0; h < NH; ++h) ring.step();                    // K(0)
-                        for (int j = 0; j < p.tiles && ok; ++j, ++use) {
-                            if (j + 1 < p.tiles)
-                                for (int h = 0; h < NH; ++h) ring.step();            // K(j + 1)
-                            // (the weights are there, so the buffers in front of V(j) are filled)
-                            ok = fm::wait_warp(p_full + 16u * (use & 1u), (use >> 1) & 1u);
-                            uint32_t b[NH];
-#pragma unroll
-                            for (int h = 0; h < NH; ++h) {
-                                b[h] = ring.at;
-                                ok = ok && fm::wait_warp(full + 8u * ring.at, ring.parity);
-                                ring.step();
-                            }
-                            if (j == 0 && finished > 0) ok = ok && fm::wait_warp(o_free, (finished - 1) & 1u);
-#pragma unroll
-                            for (int g = 0; g < 2; ++g) {
-                                if (g == 1) ok = ok && fm::wait_warp(p_full + 16u * (use & 1u) + 8u, (use >> 1) & 1u);
-                                if (!ok) break;
-                                tc::fence_after_sync();
-#pragma unroll
-                                for (int h = 0; h < NH; ++h) {
-                                    pv(0, (int)(use & 1u), h, b[h], g, j > 0 || g > 0);
-                                    if (g == 1) fm::commit(lead, empty + 8u * b[h]);
-                                }
-                                fm::commit(lead, o_done + 8u * g);
-                            }
-                            if (ok) fm::commit(lead, s_free + 8u * (use & 1u));
+                            tc::fence_after_sync();
+                            qk(0, (int)(use & 1u), h, kr.at, 0, id_qk);
+                            fm::commit(lead, empty + 8u * kr.at);
+                            kr.step();
                         }
                         if (!ok) break;
-                        fm::commit(lead, o_last);
-                        ++finished;
+                        for (int g = 0; g < 2; ++g) fm::commit(lead, s_full + 8u * (2 * (use & 1u) + g));
+                        if (j + 1 == p.tiles) fm::commit(lead, q_free);
                     }
+                } else {
+                    for (int j = 0; j < p.tiles && ok; ++j, ++use) {
+                        uint32_t b[NH];
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) {
+                            b[h] = vr.at;
+                            ok = ok && fm::wait_warp(v_full + 8u * vr.at, vr.parity);
+                            vr.step();
+                        }
+                        if (j == 0 && finished > 0) ok = ok && fm::wait_warp(o_free, (finished - 1) & 1u);
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            ok = ok && fm::wait_warp(p_full + 16u * (use & 1u) + 8u * g, (use >> 1) & 1u);
+                            if (!ok) break;
+                            tc::fence_after_sync();
+#pragma unroll
+                            for (int h = 0; h < NH; ++h) {
+                                pv(0, (int)(use & 1u), h, C::NK + b[h], g, j > 0 || g > 0);
+                                if (g == 1) fm::commit(lead, v_empty + 8u * b[h]);
+                            }
+                            fm::commit(lead, o_done + 8u * g);
+                        }
+                        if (ok) fm::commit(lead, s_free + 8u * (use & 1u));
+                    }
+                    if (!ok) break;
+                    fm::commit(lead, o_last);
+                    ++finished;
                 }
             }
             if (!ok) {
@@ -687,163 +670,139 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
         }
         __syncwarp();
     } else if (warp >= 4 * WGS) {
-        // ---- unpacking: two threads have row r of every buffer, half its blocks
-        // each (one thread a row leaves a scheduler with one unpacking warp, which
-        // waits for its own results: 8 x 128K ONETHREAD ms, with two TWOTHREADS) ----
+        // ---- unpacking: one warpgroup the keys, one the values (side by side
+        // rather than on the same tile, so that one looks up while the other waits
+        // or copies); thread r has row r of every buffer ----
         regs_down<C::R_UNPACK>();
-        const int u = tid - 128 * WGS, r = u & (kTile - 1), side = u >> 7;
-        // items of a part, in the order that the MMAs take them: step j has the
-        // key tile j and the value tile j - LEAD
-        int step = 0, half = 0, what = 0;
-        bool more = it.next(a, p);
+        const int r = tid & (kTile - 1);
+        const bool values = warp >= 4 * (WGS + 1);
+        const int bits = values ? a.v_bits : a.k_bits;
+        const uint32_t * codes = values ? a.v_codes : a.k_codes;
+        const uint16_t * norms = values ? a.v_norms : a.k_norms;
+        uint32_t tab[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) tab[i] = values ? a.v_table[i] : a.k_table[i];
+        const uint32_t packed = sbase + (uint32_t)(C::OFF_PACKED + (values ? C::PACKED : 0));
+        const unsigned char * src = smem + C::OFF_PACKED + (values ? C::PACKED : 0);
+        const uint32_t ring0 = values ? C::NK : 0u, n_ring = values ? C::NV : C::NK;
+
         // Cache row of this thread's token in key tile `tile` of the part, kNone
-        // past the last token.  (32 bits: the host refuses larger storage.)
+        // past the last token (32 bits: the host refuses larger storage); its page
+        // was read a tile earlier, the read takes a while.
         constexpr uint32_t kNone = 0xFFFFFFFFu;
-        auto page_of = [&](int t) { return __ldg(a.table + (int64_t)p.b * a.max_pages + (t >> a.page_shift)); };
-        auto row_of = [&](int page, int t) {
-            const uint32_t pg = (uint32_t)min(max(page, 0), a.n_pages - 1);
-            return ((pg * (uint32_t)a.n_kv_heads + (uint32_t)p.hk) << a.page_shift) + ((uint32_t)t & ((1u << a.page_shift) - 1u));
-        };
-        // (its page was read a step earlier: the read takes as long as half a step)
         int page = 0;
         auto read_page = [&](int tile) {
             const int t = (p.tile0 + tile) * kTile + r;
-            if (tile < p.tiles && t < p.rq.len) page = page_of(t);
+            if (tile < p.tiles && t < p.rq.len) page = __ldg(a.table + (int64_t)p.b * a.max_pages + (t >> a.page_shift));
         };
         auto tile_row = [&](int tile) {
             const int t = (p.tile0 + tile) * kTile + r;
-            return t < p.rq.len ? row_of(page, t) : kNone;
+            const uint32_t pg = (uint32_t)min(max(page, 0), a.n_pages - 1);
+            return t >= p.rq.len ? kNone
+                                 : ((pg * (uint32_t)a.n_kv_heads + (uint32_t)p.hk) << a.page_shift) +
+                                       ((uint32_t)t & ((1u << a.page_shift) - 1u));
         };
-        uint32_t row_k = kNone, row_v = kNone;           // rows of the key and the value tile of this step
-        auto start_part = [&] {
-            read_page(0);
-            row_k = tile_row(0);
-            if (LEAD == 0) row_v = row_k;
-            read_page(1);
-        };
-        // The packed words and norms of this thread's side of a row, into slot
-        // `slot`; every thread reads back only what it copied itself.
-        const uint32_t packed = sbase + (uint32_t)C::OFF_PACKED;
-        auto fetch = [&](int slot) {
-            const uint32_t row = what == 0 ? row_k : row_v;
+        // The packed words and norms of a buffer's row on their way into shared
+        // memory; every thread reads back only what it copied itself.
+        auto fetch = [&](uint32_t row, int half) {
             const bool live = row != kNone;
             const uint64_t at = live ? row : 0u;
-            const int bits = what == 0 ? a.k_bits : a.v_bits;
-            const uint32_t * c = (what == 0 ? a.k_codes : a.v_codes) + at * (uint32_t)(D / 32 * bits) +
-                                 (uint32_t)((NH == 1 ? side : 2 * half + side) * C::NBT * bits);
-            const uint32_t dst = packed + (uint32_t)(slot * C::PACKED);
+            const uint32_t * c = codes + at * (uint32_t)(D / 32 * bits) + (uint32_t)(half * NB * bits);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (i < bits) copy_or_zero<C::CHUNK>(dst + (uint32_t)((i * 2 * kTile + u) * C::CHUNK), c + i * C::NBT, live);
-            // the word that holds the norms of these blocks
-            const uint64_t nat = at * (D / 32) + (uint32_t)(half * NB + (NB == 4 ? 2 * side : 0));
-            const uint32_t nd = dst + (uint32_t)(2 * kTile * 4 * C::CHUNK + 4 * u);
-            copy_or_zero<4>(nd, (what == 0 ? a.k_norms : a.v_norms) + nat, live);
-            if (what == 0) copy_or_zero<4>(nd + (uint32_t)(8 * kTile), a.v_norms + nat, live);
+                if (i < bits) copy_or_zero<C::CHUNK>(packed + (uint32_t)((i * kTile + r) * C::CHUNK), c + i * NB, live);
+            const uint64_t nat = at * (D / 32) + (uint32_t)(half * NB);
+            const uint32_t nd = packed + (uint32_t)(kTile * 4 * C::CHUNK + r * C::NORMS);
+            copy_or_zero<C::NORMS>(nd, norms + nat, live);
+            if (!values) copy_or_zero<C::NORMS>(nd + (uint32_t)(kTile * C::NORMS), a.v_norms + nat, live);
         };
-        auto advance = [&] {
-            if (NH == 2 && ++half < NH) return;
-            half = 0;
-            // after the keys of this step its values, if any; then the next step
-            if (what == 0 && step >= LEAD) {
-                what = 1;
-                return;
-            }
-            what = 0;
-            ++step;
-            if (LEAD == 1) row_v = row_k;
-            if (step < p.tiles) {
-                row_k = tile_row(step);
-                read_page(step + 1);
-                if (LEAD == 0) row_v = row_k;
-                return;
-            }
-            if (step < p.tiles + LEAD) {
-                what = 1;
-                return;
-            }
+        uint32_t row = kNone;
+        int step = 0, half = 0, tile = 0;                // step, half: of the item on its way
+        bool more = it.next(a, p);
+        auto start_part = [&] {
             step = 0;
-            more = it.next(a, p);
-            if (more) start_part();
+            read_page(0);
+            row = tile_row(0);
+            read_page(1);
         };
-        // Three items are on their way while one is unpacked; flags: bit 0 values,
-        // bit 1 second half.
-        fm::Ring<ST> ring;
-        int filled = 0, tile = 0, slot = 0, flags[3], left = 0;
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            flags[k] = 0;
-            if (more) {
-                if (k == 0) start_part();
-                fetch(k);
-                flags[k] = what | half << 1;
-                ++left;
-                advance();
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+        if (more) {
+            start_part();
+            fetch(row, 0);
         }
-        while (left > 0) {
-            const uint32_t s = ring.at;
-            const bool ok = filled < ST || fm::wait(empty + 8u * s, ring.parity ^ 1u);
+        uint32_t at = 0, parity = 1;                     // buffer of the ring, parity of its last release
+        while (more) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            uint32_t w[4 * NB], norm[NB / 2], other[NB / 2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (NB == 4) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(src + (i * kTile + r) * 16);
+                    w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(src + (i * kTile + r) * 8);
+                    w[2 * i] = x.x; w[2 * i + 1] = x.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NB / 2; ++i) {
+                const uint32_t * n = reinterpret_cast<const uint32_t *>(src + kTile * 4 * C::CHUNK + r * C::NORMS) + i;
+                norm[i] = n[0];
+                other[i] = n[kTile * C::NORMS / 4];
+            }
+            // a key with an infinite or NaN norm marks its readers' sums, and takes
+            // no part in the products
+            uint32_t bad = 0u;
+#pragma unroll
+            for (int i = 0; i < NB / 2; ++i)
+                bad |= ((norm[i] & 0x7C007C00u) + 0x04000400u) | (values ? 0u : (other[i] & 0x7C007C00u) + 0x04000400u);
+            bad &= 0x80008000u;
+            const int this_half = half;
+            if (!values) {
+                const uint32_t keys = __ballot_sync(0xffffffffu, bad != 0u);
+                if (lane == 0) {
+                    volatile uint32_t * word = s_bad + 4 * (tile & 7) + (warp - 4 * WGS);
+                    *word = this_half == 0 ? keys : *word | keys;
+                }
+                if (this_half == NH - 1) ++tile;
+            }
+            if (bad != 0u) {
+#pragma unroll
+                for (int i = 0; i < NB / 2; ++i) norm[i] = 0u;
+            }
+            // the next item
+            if (NH == 2 && half == 0) {
+                half = 1;
+            } else {
+                half = 0;
+                if (++step < p.tiles) {
+                    row = tile_row(step);
+                    read_page(step + 1);
+                } else {
+                    more = it.next(a, p);
+                    if (more) start_part();
+                }
+            }
+            if (more) fetch(row, half);
+            // (a fresh barrier counts as released: its phase before the first has parity 1)
+            const uint32_t s = ring0 + at;
+            const bool ok = fm::wait(empty + 8u * s, parity);
             if (!__all_sync(0xffffffffu, ok)) {
                 *s_err = 1;
                 break;
             }
-            asm volatile("cp.async.wait_group 2;" ::: "memory");
-            const unsigned char * src = smem + C::OFF_PACKED + slot * C::PACKED;
-            uint32_t w[4 * C::NBT];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (C::NBT == 2) {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(src + (i * 2 * kTile + u) * 8);
-                    w[2 * i] = x.x; w[2 * i + 1] = x.y;
-                } else {
-                    w[i] = *reinterpret_cast<const uint32_t *>(src + (i * 2 * kTile + u) * 4);
-                }
-            }
-            const uint32_t * nw = reinterpret_cast<const uint32_t *>(src + 2 * kTile * 4 * C::CHUNK) + u;
-            uint32_t norm = nw[0];
-            const uint32_t other = nw[2 * kTile];
-            const int item = flags[0];
-            flags[0] = flags[1];
-            flags[1] = flags[2];
-            --left;
-            // a key with an infinite or NaN norm marks its readers' sums, and takes
-            // no part in the products
-            const uint32_t bad = (((norm & 0x7C007C00u) + 0x04000400u) | (item & 1 ? 0u : (other & 0x7C007C00u) + 0x04000400u)) & 0x80008000u;
-            if ((item & 1) == 0) {
-                const uint32_t keys = __ballot_sync(0xffffffffu, bad != 0u);
-                if (lane == 0) {
-                    volatile uint32_t * word = s_bad + 8 * (tile & 7) + (warp - 4 * WGS);
-                    *word = item == 0 ? keys : *word | keys;
-                }
-                if (NH == 1 || item != 0) ++tile;
-            }
-            if (bad != 0u) norm = 0u;
-            if (NB == 2) norm = side ? norm >> 16 : norm;
-            if (more) {
-                fetch(slot);
-                flags[2] = what | half << 1;
-                ++left;
-                advance();
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            slot = slot == 2 ? 0 : slot + 1;
             unsigned char * dst = smem + C::OFF_RING + s * C::BUF + r * 128;
-            const int bits = item & 1 ? a.v_bits : a.k_bits;
-            uint32_t tab[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) tab[i] = item & 1 ? a.v_table[i] : a.k_table[i];
-            if (bits == 4) unpack_row<4, C::NBT>(w, norm, tab, dst, side, r & 7);
-            else if (bits == 3) unpack_row<3, C::NBT>(w, norm, tab, dst, side, r & 7);
-            else unpack_row<2, C::NBT>(w, norm, tab, dst, side, r & 7);
+            if (bits == 4) unpack_row<4, NB>(w, norm, tab, dst, r & 7);
+            else if (bits == 3) unpack_row<3, NB>(w, norm, tab, dst, r & 7);
+            else unpack_row<2, NB>(w, norm, tab, dst, r & 7);
             tc::fence_proxy_async();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(full + 8u * s);
-            ring.step();
-            if (filled < ST) ++filled;
+            if (++at == n_ring) {
+                at = 0;
+                parity ^= 1u;
+            }
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         // ---- softmax: warpgroup w, one thread per row ----
         regs_up<C::R_SOFTMAX>();
@@ -911,8 +870,8 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                         const uint32_t al[2] = {g == 0 ? allowed[0] : allowed[2], g == 0 ? allowed[1] : allowed[3]};
                         if (edge) ok = fm::softmax_half<false, true>(half, first && g == 0, mul, al, st, scale_acc);
                         else ok = fm::softmax_half<false, false>(half, first && g == 0, mul, nullptr, st, scale_acc);
-                        const volatile uint32_t * bad = s_bad + 8 * ((tile0 + j) & 7) + 2 * g;
-                        if ((((bad[0] | bad[4]) & al[0]) | ((bad[1] | bad[5]) & al[1])) != 0u) st.sum = CUDART_NAN_F;
+                        const volatile uint32_t * bad = s_bad + 4 * ((tile0 + j) & 7) + 2 * g;
+                        if (((bad[0] & al[0]) | (bad[1] & al[1])) != 0u) st.sum = CUDART_NAN_F;
                     }
                     tc::mbar_arrive(p_full + 8u * (2 * slot + g));
                 }
