@@ -389,12 +389,36 @@ def _dtype_code16(t):
     return DTYPES["f16"] if t.dtype == torch.float16 else _dtype_code(t)
 
 
-def _int_array(t, n, name, device, kind="int32"):
-    """A contiguous integer array of n entries on ``device`` (the kernels read
-    it without further checks)."""
+def _ints(t, n, name, device, kind):
+    """Pointer of a contiguous integer array of n entries on ``device`` (the
+    kernels read it without further checks)."""
+    if not (t.dtype is kind and t.numel() == n and t.is_contiguous() and t.device == device):
+        raise ValueError(f"{name}: contiguous {kind} of {n} entries on {device}")
+    return t.data_ptr()
+
+
+def _host_floats(x):
+    """(array that keeps it alive, pointer) of a contiguous fp32 copy or view of
+    x (``ndarray.ctypes`` builds an object a call, several times slower)."""
+    a = np.ascontiguousarray(x, dtype=np.float32)
+    return a, a.__array_interface__["data"][0]
+
+
+def _launch(fn, where, device, stream, *args):
+    """fn(*args, stream) with ``device`` current (as _on; a serving step makes
+    many short calls, so nothing is switched that is current already)."""
     import torch
-    _require(t.dtype == getattr(torch, kind) and t.is_contiguous() and t.numel() == n and
-             t.device == device, f"{name}: contiguous {kind} of {n} entries on {device}")
+    if device.type != "cuda":
+        raise ValueError(f"{where}: tensors on {device}, not on a CUDA device")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream.cuda_stream)
+    if status != 0:
+        raise TQError(status, where)
 
 
 def page_tables(ctx_lens, new_lens, page_size, n_pages, free_pages, block_table, n_slots, out=None,
@@ -417,24 +441,19 @@ def page_tables(ctx_lens, new_lens, page_size, n_pages, free_pages, block_table,
                "slots": torch.empty((n_slots,), dtype=torch.int64, device=dev),
                "positions": torch.empty((n_slots,), dtype=torch.int32, device=dev),
                "n_taken": torch.empty((1,), dtype=torch.int32, device=dev)}
-    _int_array(ctx_lens, batch, "ctx_lens", dev)
-    _int_array(new_lens, batch, "new_lens", dev)
-    _int_array(free_pages, free_pages.numel(), "free_pages", dev)
-    _int_array(out["cu_new"], batch + 1, "cu_new", dev)
-    _int_array(out["total_lens"], batch, "total_lens", dev)
-    _int_array(out["slots"], n_slots, "slots", dev, "int64")
-    _int_array(out["n_taken"], 1, "n_taken", dev)
-    positions = out.get("positions")
-    if positions is not None:
-        _int_array(positions, n_slots, "positions", dev)
+    i32 = torch.int32
     _require(block_table.dim() == 2 and block_table.shape[0] == batch, "block_table: [batch, max_pages]")
-    _int_array(block_table, block_table.numel(), "block_table", dev)
-    with _on(dev):
-        _check(_lib.tq_page_tables(
-            _ptr(ctx_lens), _ptr(new_lens), batch, page_size, n_pages, _ptr(free_pages),
-            free_pages.numel(), _ptr(block_table), block_table.shape[1], _ptr(out["cu_new"]),
-            _ptr(out["total_lens"]), _ptr(out["slots"]), _ptr(positions), n_slots,
-            _ptr(out["n_taken"]), _ptr(status), _stream_ptr(stream, dev)), "tq_page_tables")
+    n_free, max_pages = free_pages.numel(), block_table.shape[1]
+    positions = out.get("positions")
+    args = (_ints(ctx_lens, batch, "ctx_lens", dev, i32), _ints(new_lens, batch, "new_lens", dev, i32), batch,
+            page_size, n_pages, _ints(free_pages, n_free, "free_pages", dev, i32), n_free,
+            _ints(block_table, batch * max_pages, "block_table", dev, i32), max_pages,
+            _ints(out["cu_new"], batch + 1, "cu_new", dev, i32),
+            _ints(out["total_lens"], batch, "total_lens", dev, i32),
+            _ints(out["slots"], n_slots, "slots", dev, torch.int64),
+            None if positions is None else _ints(positions, n_slots, "positions", dev, i32), n_slots,
+            _ints(out["n_taken"], 1, "n_taken", dev, i32), _ptr(status))
+    _launch(_lib.tq_page_tables, "tq_page_tables", dev, stream, *args)
     return out
 
 
@@ -449,21 +468,19 @@ def quantize_kv_paged(rot, bits, centroids, boundaries, x, slots, codes, norms, 
     n, heads, d = x.shape
     dev = x.device
     n_pages = codes.shape[0]
-    w = max(code_words_per_row(bits, block, d), 0)
+    w = d * bits // 32                                  # (the library refuses other blocks and widths)
     _require(x.is_contiguous(), "x: contiguous [n_tokens, n_kv_heads, head_dim]")
-    _int_array(slots, n, "slots", dev, "int64")
+    slots_p = _ints(slots, n, "slots", dev, torch.int64)
     _require(tuple(codes.shape) == (n_pages, heads, page_size, w) and codes.dtype == torch.int32 and
              codes.is_contiguous() and codes.device == dev, f"codes: int32 [n_pages, {heads}, {page_size}, {w}]")
     _require(tuple(norms.shape) == (n_pages, heads, page_size, d // 32) and norms.dtype == torch.int16 and
              norms.is_contiguous() and norms.device == dev,
              f"norms: int16 [{n_pages}, {heads}, {page_size}, {d // 32}]")
-    c = np.ascontiguousarray(centroids, dtype=np.float32)
-    t = np.ascontiguousarray(boundaries, dtype=np.float32)
-    with _on(dev):
-        _check(_lib.tq_quantize_kv_paged(
-            rot.handle, bits, block, c.ctypes.data, t.ctypes.data, _ptr(x), _dtype_code(x), n, heads,
-            d, _ptr(slots), page_size, n_pages, _ptr(codes), _ptr(norms), _ptr(status),
-            _stream_ptr(stream, dev)), "tq_quantize_kv_paged")
+    c, c_p = _host_floats(centroids)
+    t, t_p = _host_floats(boundaries)
+    _launch(_lib.tq_quantize_kv_paged, "tq_quantize_kv_paged", dev, stream, rot.handle, bits, block, c_p,
+            t_p, _ptr(x), _dtype_code(x), n, heads, d, slots_p, page_size, n_pages, _ptr(codes), _ptr(norms),
+            _ptr(status))
 
 
 def prompt_attention(q, k, v, cu_q, cu_k=None, scale=0.0, out=None, status=None, stream=None):
@@ -486,17 +503,15 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, scale=0.0, out=None, status=None,
     _require(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous() and out.device == dev,
              "out: contiguous, of q's shape and type")
     batch = cu_q.numel() - 1
-    _int_array(cu_q, batch + 1, "cu_q", dev)
+    cu_q_p = _ints(cu_q, batch + 1, "cu_q", dev, torch.int32)
+    cu_k_p = None
     if cu_k is not None:
-        _int_array(cu_k, batch + 1, "cu_k", dev)
+        cu_k_p = _ints(cu_k, batch + 1, "cu_k", dev, torch.int32)
     else:
         _require(total_k == total_q, "cu_k is needed where k has another length than q")
     strides = [t.stride(0) if t.shape[0] > 1 else t.shape[1] * d for t in (q, k, v)]
-    with _on(dev):
-        _check(_lib.tq_prompt_attention(
-            _ptr(q), _ptr(k), _ptr(v), _dtype_code16(q), _ptr(cu_q), _ptr(cu_k), batch, total_q,
-            total_k, n_q, n_kv, d, *strides, float(scale), _ptr(out), _ptr(status),
-            _stream_ptr(stream, dev)), "tq_prompt_attention")
+    _launch(_lib.tq_prompt_attention, "tq_prompt_attention", dev, stream, _ptr(q), _ptr(k), _ptr(v), _dtype_code16(q),
+            cu_q_p, cu_k_p, batch, total_q, total_k, n_q, n_kv, d, *strides, float(scale), _ptr(out), _ptr(status))
     return out
 
 
@@ -524,37 +539,34 @@ def tree_attention(rot, k_bits, v_bits, k_centroids, v_centroids, q, cu_nodes, l
         out = torch.empty((n_rows, n_q, d), dtype=q.dtype, device=dev)
     _require(q.is_contiguous() and out.shape == q.shape and out.dtype == q.dtype and
              out.is_contiguous() and out.device == dev, "q and out: contiguous, same shape and type")
-    _int_array(cu_nodes, batch + 1, "cu_nodes", dev)
-    _int_array(lens, batch, "lens", dev)
+    cu_p = _ints(cu_nodes, batch + 1, "cu_nodes", dev, torch.int32)
+    lens_p = _ints(lens, batch, "lens", dev, torch.int32)
     _require(block_table.dim() == 2 and block_table.shape[0] == batch, "block_table: [batch, max_pages]")
-    _int_array(block_table, block_table.numel(), "block_table", dev)
+    table_p = _ints(block_table, batch * block_table.shape[1], "block_table", dev, torch.int32)
     n_pages, n_kv = pages["k_codes"].shape[:2]
     for name, bits in (("k", k_bits), ("v", v_bits)):
         c, n = pages[name + "_codes"], pages[name + "_norms"]
-        w = max(code_words_per_row(bits, block, d), 0)
+        w = d * bits // 32                              # (the library refuses other blocks and widths)
         _require(tuple(c.shape) == (n_pages, n_kv, page_size, w) and c.dtype == torch.int32 and
                  c.is_contiguous() and c.device == dev,
                  f"{name}_codes: int32 [{n_pages}, {n_kv}, {page_size}, {w}]")
         _require(tuple(n.shape) == (n_pages, n_kv, page_size, d // 32) and n.dtype == torch.int16 and
                  n.is_contiguous() and n.device == dev,
                  f"{name}_norms: int16 [{n_pages}, {n_kv}, {page_size}, {d // 32}]")
-    words = 0
+    words, mask_p = 0, None
     if tree_mask is not None:
         _require(tree_mask.dim() == 2, "tree_mask: [n_rows, words]")
         words = tree_mask.shape[1]
-        _int_array(tree_mask, n_rows * words, "tree_mask", dev, "int64")
-    kc = np.ascontiguousarray(k_centroids, dtype=np.float32)
-    vc = np.ascontiguousarray(v_centroids, dtype=np.float32)
-    with _on(dev):
-        if workspace is None:
+        mask_p = _ints(tree_mask, n_rows * words, "tree_mask", dev, torch.int64)
+    kc, kc_p = _host_floats(k_centroids)
+    vc, vc_p = _host_floats(v_centroids)
+    if workspace is None:
+        with _on(dev):
             need = tree_workspace_size(batch, n_rows, max_nodes, n_q, n_kv, max_len, d)
             workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
-        _check(_lib.tq_tree_attention(
-            rot.handle, k_bits, v_bits, block, kc.ctypes.data, vc.ctypes.data, _ptr(q),
-            _dtype_code16(q), _ptr(cu_nodes), batch, n_rows, max_nodes, _ptr(lens), max_len,
-            _ptr(tree_mask), words, n_q, n_kv, d, page_size, n_pages, _ptr(block_table),
-            block_table.shape[1], _ptr(pages["k_codes"]), _ptr(pages["k_norms"]),
-            _ptr(pages["v_codes"]), _ptr(pages["v_norms"]), float(scale), _ptr(out),
-            _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
-            _stream_ptr(stream, dev)), "tq_tree_attention")
+    _launch(_lib.tq_tree_attention, "tq_tree_attention", dev, stream, rot.handle, k_bits, v_bits, block, kc_p,
+            vc_p, _ptr(q), _dtype_code16(q), cu_p, batch, n_rows, max_nodes, lens_p, max_len, mask_p, words,
+            n_q, n_kv, d, page_size, n_pages, table_p, block_table.shape[1], _ptr(pages["k_codes"]),
+            _ptr(pages["k_norms"]), _ptr(pages["v_codes"]), _ptr(pages["v_norms"]), float(scale), _ptr(out),
+            _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status))
     return out
