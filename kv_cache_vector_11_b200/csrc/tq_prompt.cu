@@ -77,7 +77,7 @@ struct PaCfg {
     // for it
     static constexpr int N_BAR = 2 * STAGES + 20;
     static constexpr int OFF_MISC = OFF_BAR + 8 * N_BAR;
-    static constexpr int SMEM = OFF_MISC + 32 + 8 * (THREADS / 32) + 1024;   // + alignment of the base
+    static constexpr int SMEM = OFF_MISC + 32 + 4 * (THREADS / 32) + 1024;   // + alignment of the base
     static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
@@ -86,7 +86,7 @@ __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ void from_f32(float x, __nv_bfloat16 * o) { *o = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void from_f32(float x, __half * o) { *o = __float2half_rn(x); }
 
-__device__ __forceinline__ int64_t clamp_to(int64_t x, int64_t lo, int64_t hi) { return min(max(x, lo), hi); }
+__device__ __forceinline__ int clamp_to(int x, int lo, int hi) { return min(max(x, lo), hi); }
 
 // One row by one warp on the CUDA cores: the first n keys from row k0 on.
 template <int D, typename T>
@@ -141,58 +141,98 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     volatile int * s_err = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
     volatile int * s_redo = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8);
     int * s_seq = reinterpret_cast<int *>(smem + C::OFF_MISC + 12);      // sequence, tile
-    int64_t * s_sums = reinterpret_cast<int64_t *>(smem + C::OFF_MISC + 32);
+    int * s_sums = reinterpret_cast<int *>(smem + C::OFF_MISC + 32);
 
-    // which sequence and tile: the tiles of all sequences are counted one
-    // sequence after another; blocks of one tile and all heads follow each other
-    const int n_groups = a.n_q_heads / a.heads;
-    const int64_t tau = blockIdx.x / (unsigned)n_groups;
-    const int hg = (int)(blockIdx.x - (unsigned)tau * (unsigned)n_groups);
-    const int cta_queries = NQ * a.queries;
+    // Barriers and TMEM first: a block's way to its first product is 3 us, a fifth
+    // of the time of 16 prompts of 64 .. 2048 tokens.
     if (tid == 0) {
-        s_seq[0] = -1;
+        tc::mbar_init(q_full, 1);
+        for (int i = 0; i < ST; ++i) {
+            tc::mbar_init(full + 8u * i, 1);
+            tc::mbar_init(empty + 8u * i, NQ);
+        }
+        for (int i = 0; i < 4; ++i) {
+            tc::mbar_init(s_full + 8u * i, 1);
+            tc::mbar_init(p_full + 8u * i, 128);
+            tc::mbar_init(o_done + 8u * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(o_last + 8u * i, 1);
+            tc::mbar_init(s_free + 8u * i, 1);
+            tc::mbar_init(drained + 8u * i, 1);
+        }
+        tc::mbar_init(scanned, 32);
         *s_err = 0;
         *s_redo = 0;
+        s_seq[0] = -1;
     }
-    int64_t before = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += NT) {
-        const int b = b0 + tid;
-        int64_t n = 0;
-        if (b < a.batch) {
-            const int64_t r0 = clamp_to(a.cu_q[b], 0, a.total_q), r1 = clamp_to(a.cu_q[b + 1], r0, a.total_q);
-            n = (r1 - r0 + cta_queries - 1) / cta_queries;
-        }
-        int64_t incl = n;
+
+    // Which sequence and tile: the tiles of all sequences are counted one sequence
+    // after another, a sequence's last tile first (it has the most keys); blocks of
+    // one tile and all heads follow each other.
+    const int n_groups = a.n_q_heads / a.heads;
+    const int tau = (int)(blockIdx.x / (unsigned)n_groups);
+    const int hg = (int)(blockIdx.x - (unsigned)tau * (unsigned)n_groups);
+    const int cta_queries = NQ * a.queries;
+    auto tiles_of = [&](int b) {
+        if (b >= a.batch) return 0;
+        const int r0 = clamp_to(a.cu_q[b], 0, (int)a.total_q), r1 = clamp_to(a.cu_q[b + 1], r0, (int)a.total_q);
+        return (int)((unsigned)(r1 - r0 + cta_queries - 1) / (unsigned)cta_queries);
+    };
+    auto warp_scan = [&](int n) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += u;
+            const int u = __shfl_up_sync(0xffffffffu, n, o);
+            if (lane >= o) n += u;
         }
-        __syncthreads();
-        if (lane == 31) s_sums[warp] = incl;
-        __syncthreads();
-        int64_t all = 0;
+        return n;
+    };
+    int seq = -1, tile = 0;
+    if (a.batch <= 128) {
+        // every warp for itself, without a barrier
+        int before = 0;
+        for (int b0 = 0; b0 < a.batch && seq < 0; b0 += 32) {
+            const int n = tiles_of(b0 + lane);
+            const int end = before + warp_scan(n);
+            const unsigned hit = __ballot_sync(0xffffffffu, tau < end);
+            if (hit != 0u) {
+                const int at = __ffs((int)hit) - 1;
+                seq = b0 + at;
+                tile = __shfl_sync(0xffffffffu, end, at) - 1 - tau;
+            }
+            before = __shfl_sync(0xffffffffu, end, 31);
+        }
+    } else {
+        int before = 0;
+        for (int b0 = 0; b0 < a.batch && before <= tau; b0 += NT) {
+            const int n = tiles_of(b0 + tid);
+            int end = warp_scan(n);
+            __syncthreads();
+            if (lane == 31) s_sums[warp] = end;
+            __syncthreads();
+            int all = 0;
 #pragma unroll
-        for (int w = 0; w < NT / 32; ++w) {
-            const int64_t s = s_sums[w];
-            if (w < warp) incl += s;
-            all += s;
+            for (int w = 0; w < NT / 32; ++w) {
+                const int x = s_sums[w];
+                if (w < warp) end += x;
+                all += x;
+            }
+            end += before;
+            if (tau < end && tau >= end - n) {
+                s_seq[0] = b0 + tid;
+                s_seq[1] = end - 1 - tau;
+            }
+            before += all;
         }
-        incl += before;
-        if (tau < incl && tau >= incl - n) {
-            s_seq[0] = b;
-            s_seq[1] = (int)(incl - 1 - tau);            // the last tile first: it has the most keys
-        }
-        before += all;
-        if (before > tau) break;
+        __syncthreads();
+        seq = s_seq[0];
+        tile = s_seq[1];
     }
-    __syncthreads();
-    const int seq = s_seq[0];
     if (seq < 0) return;                                  // past the last tile
-    const int64_t q0 = clamp_to(a.cu_q[seq], 0, a.total_q), q1 = clamp_to(a.cu_q[seq + 1], q0, a.total_q);
-    const int64_t k0 = clamp_to(a.cu_k[seq], 0, a.total_k), k1 = clamp_to(a.cu_k[seq + 1], k0, a.total_k);
-    const int nq = (int)(q1 - q0), nk = (int)(k1 - k0);
-    const int i0 = s_seq[1] * cta_queries;                // first query of this CTA
+    const int q0 = clamp_to(a.cu_q[seq], 0, (int)a.total_q), q1 = clamp_to(a.cu_q[seq + 1], q0, (int)a.total_q);
+    const int k0 = clamp_to(a.cu_k[seq], 0, (int)a.total_k), k1 = clamp_to(a.cu_k[seq + 1], k0, (int)a.total_k);
+    const int nq = q1 - q0, nk = k1 - k0;
+    const int i0 = tile * cta_queries;                    // first query of this CTA
     const int shift = nk - nq;                            // query i attends the keys below i + shift + 1
     const int i_last = min(i0 + cta_queries, nq) - 1;
     const int n_keys = max(i_last + shift + 1, 0);        // (at most nk)
@@ -203,24 +243,6 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     const int h0 = hg * a.heads, hk = h0 / (a.n_q_heads / a.n_kv_heads);
 
     if (n > 0) {
-        if (tid == 0) {
-            tc::mbar_init(q_full, 1);
-            for (int i = 0; i < ST; ++i) {
-                tc::mbar_init(full + 8u * i, 1);
-                tc::mbar_init(empty + 8u * i, NQ == 1 ? 1 : slots);
-            }
-            for (int i = 0; i < 4; ++i) {
-                tc::mbar_init(s_full + 8u * i, 1);
-                tc::mbar_init(p_full + 8u * i, 128);
-                tc::mbar_init(o_done + 8u * i, 1);
-            }
-            for (int i = 0; i < 2; ++i) {
-                tc::mbar_init(o_last + 8u * i, 1);
-                tc::mbar_init(s_free + 8u * i, 1);
-                tc::mbar_init(drained + 8u * i, 1);
-            }
-            tc::mbar_init(scanned, 32);
-        }
         if (warp == 0) tc::tmem_alloc(sbase + (uint32_t)C::OFF_MISC, 512);
         tc::fence_before_sync();
         __syncthreads();
@@ -237,11 +259,11 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             for (int i = 0; i < slots; ++i)
                 for (int c = 0; c < D / 64; ++c)
                     tc::tma_load_3d(sbase + (uint32_t)((i * (D / 64) + c) * C::SLICE), &qmap, 64 * c, h0,
-                                    (int)(q0 + i0 + i * a.queries), q_full);
+                                    q0 + i0 + i * a.queries, q_full);
             int it = 0;
             bool ok = true;
             for (int j = 0; j < n && ok; ++j) {
-                const int key = (int)k0 + (n - 1 - j) * kTile;
+                const int key = k0 + (n - 1 - j) * kTile;
 #pragma unroll 1
                 for (int kv = 0; kv < 2 && ok; ++kv) {
                     const CUtensorMap * map = kv == 0 ? &kmap : &vmap;
@@ -301,6 +323,10 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             if constexpr (NQ == 2) {
                 // thread t: row tile t.  The scores of a half come behind the
                 // products that read the weights they overwrite.
+                auto release = [&](uint32_t b) {              // for the other thread too, if it has no share
+                    fm::commit(lead, empty + 8u * b);
+                    if (slots == 1) fm::commit(lead, empty + 8u * b);
+                };
                 const uint32_t sf = s_full + 16u * t, pf = p_full + 16u * t, od = o_done + 16u * t;
                 ok = ok && fm::wait_warp(full, 0u);
                 if (ok) {
@@ -308,7 +334,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                         qk(t, t, 0, 0u, 64 * g, id_qk64);
                         fm::commit(lead, sf + 8u * g);
                     }
-                    fm::commit(lead, empty);
+                    release(0u);
                 }
                 ring.step();
                 for (int j = 0; j < n && ok; ++j) {
@@ -336,10 +362,10 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     if (more) {
                         qk(t, t, 0, k, 64, id_qk64);
                         fm::commit(lead, sf + 8u);
-                        fm::commit(lead, empty + 8u * k);
+                        release(k);
                     }
                     fm::commit(lead, od + 8u);
-                    fm::commit(lead, empty + 8u * v);
+                    release(v);
                 }
                 if (ok) fm::commit(lead, o_last + 8u * t);
             } else if (t == 0) {
@@ -441,7 +467,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         const int qi = i0 + i * a.queries + qt;
         const bool valid = qt < a.queries && qi < nq;
         const int lim = valid ? min(max(qi + shift + 1, 0), nk) : 0;      // keys of this row
-        T * op = static_cast<T *>(a.out) + ((q0 + qi) * a.n_q_heads + h0 + g) * D;
+        T * op = static_cast<T *>(a.out) + ((int64_t)(q0 + qi) * a.n_q_heads + h0 + g) * D;
         if (n > 0 && i < slots) {
             const uint32_t lane_tm = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
             const uint32_t o_tm = lane_tm + fm::kOutCol + (uint32_t)(i * D);
