@@ -196,15 +196,25 @@ __device__ __forceinline__ void warp_fwht(float * v, int lane) {
     for (int i = 0; i < E; ++i) v[i] *= sc;
 }
 
-// The request of a row: the last one that starts at or before it.
-__device__ __forceinline__ int request_of_row(const TreeArgs & a, int row) {
-    int lo = 0, hi = a.batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu[mid] <= row) lo = mid; else hi = mid;
+// The request of a row, the last one that starts at or before it, by a whole
+// warp: 32 starts a step (one read in sequence for up to 32 requests, two for up
+// to 1024).
+__device__ __forceinline__ int request_of_row(const TreeArgs & a, int row, int lane) {
+    int lo = 0, n = a.batch;
+    while (n > 1) {
+        const int step = (n + 31) >> 5, at = lo + lane * step;
+        const unsigned before = __ballot_sync(0xffffffffu, lane * step < n && a.cu[min(at, a.batch)] <= row);
+        const int k = max(__popc(before) - 1, 0) * step;
+        lo += k;
+        n = min(step, n - k);
     }
     return lo;
 }
+
+// Programmatic dependent launch: the next kernel of the stream may start its
+// prologue / the kernel in front is complete and its results are visible.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Block 0: the units before every request.  The others: one warp per (row,
 // head), q~ = R q times a power of two that brings the row's largest
@@ -216,6 +226,7 @@ __global__ void __launch_bounds__(kTpThreads) tree_prep_kernel(const __grid_cons
     __shared__ float x_s[NW][D];
     __shared__ int64_t sums[NW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    let_next_start();
     if (blockIdx.x == 0) {
         int64_t before = 0;
         for (int b0 = 0; b0 < a.batch; b0 += kTpThreads) {
@@ -249,7 +260,7 @@ __global__ void __launch_bounds__(kTpThreads) tree_prep_kernel(const __grid_cons
     const int64_t vec = (int64_t)(blockIdx.x - 1) * NW + warp;
     if (vec >= (int64_t)a.n_rows * a.n_q_heads) return;
     const int row = (int)(vec / a.n_q_heads), h = (int)(vec - (int64_t)row * a.n_q_heads);
-    const Request q = request_of(a, request_of_row(a, row));
+    const Request q = request_of(a, request_of_row(a, row, lane));
     const int node = row - q.r0;
     if (node < 0 || node >= q.n) return;
     float v[E];
@@ -476,6 +487,8 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
         *s_err = 0;
     }
     if (warp == 0) tc::tmem_alloc(sbase + (uint32_t)C::OFF_MISC, 512);
+    let_next_start();
+    wait_for_previous();
     {
         // the request of this CTA's first unit
         const int64_t units = a.unit0[a.batch], u0 = first_unit(blockIdx.x, units, sharers(a, units));
@@ -497,6 +510,8 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
         // products; a third warp loads the row tiles ----
         const int t = warp - 4 * (WGS + 2);
         if (t == 2 && lane == 0) {
+            // (the rotated rows were written by plain stores of the kernel in front)
+            asm volatile("fence.proxy.async;" ::: "memory");
             bool ok = true;
             for (int part = 0; ok && it.next(a, p); ++part) {
                 if (part > 0) ok = fm::wait(q_free, (uint32_t)((part - 1) & 1));
@@ -923,15 +938,16 @@ __global__ void __launch_bounds__(kTmThreads) tree_combine_kernel(const __grid_c
     const int64_t vec = (int64_t)blockIdx.x * NW + warp;
     if (vec >= (int64_t)a.n_rows * a.n_q_heads) return;
     const int row = (int)(vec / a.n_q_heads), h = (int)(vec - (int64_t)row * a.n_q_heads);
-    const int b = request_of_row(a, row);
+    const int b = request_of_row(a, row, lane);
     const Request q = request_of(a, b);
     const int node = row - q.r0;
     if (node < 0 || node >= q.n) return;
     const int hk = h / a.group, in_req = node * a.group + h - hk * a.group;
     const int set = in_req / a.rows_per_set, in_set = in_req - set * a.rows_per_set;
     const int64_t id = (int64_t)q.r0 * a.n_q_heads + (int64_t)hk * q.n * a.group + in_req;
-    const int64_t units = a.unit0[a.batch];
     const int tiles = tiles_of(q.len);
+    wait_for_previous();
+    const int64_t units = a.unit0[a.batch];
     const int64_t u0 = a.unit0[b] + ((int64_t)hk * sets_of(a, q.n) + set) * tiles;
     float ref = -CUDART_INF_F, sum = 0.0f, v[E];
 #pragma unroll
@@ -985,6 +1001,22 @@ __global__ void __launch_bounds__(kTmThreads) tree_combine_kernel(const __grid_c
     }
 }
 
+// A launch that may start while the kernel in front of it is still running.
+template <typename K, typename... Args>
+int launch_dependent(K kernel, unsigned grid, unsigned threads, size_t smem, cudaStream_t st, const Args &... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return (int)cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int D, int MODE>
 int launch_tree_main(const TreeArgs & a, cudaStream_t st) {
     using C = TaCfg<D, MODE>;
@@ -995,8 +1027,7 @@ int launch_tree_main(const TreeArgs & a, cudaStream_t st) {
         return (int)cudaErrorInvalidValue;
     auto k = tree_kernel<D, MODE>;
     if (int e = ensure_dynamic_smem(reinterpret_cast<const void *>(k), C::SMEM)) return e;
-    k<<<(unsigned)a.n_ctas, C::THREADS, C::SMEM, st>>>(a, qmap);
-    return (int)cudaGetLastError();
+    return launch_dependent(k, (unsigned)a.n_ctas, C::THREADS, C::SMEM, st, a, qmap);
 }
 
 template <int D>
@@ -1008,8 +1039,7 @@ int launch_tree(TreeArgs & a, cudaStream_t st) {
     if constexpr (D == 256) e = launch_tree_main<D, WIDE>(a, st);
     else e = a.streams == 2 ? launch_tree_main<D, STREAM>(a, st) : launch_tree_main<D, PAIR>(a, st);
     if (e) return e;
-    tree_combine_kernel<D><<<vecs, kTmThreads, 0, st>>>(a);
-    return (int)cudaGetLastError();
+    return launch_dependent(tree_combine_kernel<D>, vecs, kTmThreads, 0, st, a);
 }
 
 // Workspace sections, each from a 256-byte boundary.
