@@ -167,6 +167,77 @@ __device__ __forceinline__ void store_el(void * p, int dt, int64_t i, float v) {
     else if (dt == TQ_DTYPE_BF16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
     else static_cast<__half *>(p)[i] = __float2half_rn(v);
 }
+// E consecutive elements from a multiple of E on (2, 4 or 8 of them), as one or
+// two wide accesses.
+template <int BYTES>
+struct Words {
+    uint32_t w[BYTES / 4];
+};
+template <int BYTES>
+__device__ __forceinline__ Words<BYTES> load_words(const void * p) {
+    Words<BYTES> r;
+    if constexpr (BYTES % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < BYTES / 16; ++i) {
+            const uint4 u = static_cast<const uint4 *>(p)[i];
+            r.w[4 * i] = u.x; r.w[4 * i + 1] = u.y; r.w[4 * i + 2] = u.z; r.w[4 * i + 3] = u.w;
+        }
+    } else if constexpr (BYTES == 8) {
+        const uint2 u = *static_cast<const uint2 *>(p);
+        r.w[0] = u.x; r.w[1] = u.y;
+    } else {
+        r.w[0] = *static_cast<const uint32_t *>(p);
+    }
+    return r;
+}
+template <int BYTES>
+__device__ __forceinline__ void store_words(void * p, const Words<BYTES> & r) {
+    if constexpr (BYTES % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < BYTES / 16; ++i)
+            static_cast<uint4 *>(p)[i] = make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
+    } else if constexpr (BYTES == 8) {
+        *static_cast<uint2 *>(p) = make_uint2(r.w[0], r.w[1]);
+    } else {
+        *static_cast<uint32_t *>(p) = r.w[0];
+    }
+}
+template <int E>
+__device__ __forceinline__ void load_vec(const void * p, int dt, int64_t at, float * v) {
+    if (dt == TQ_DTYPE_F32) {
+        const Words<4 * E> r = load_words<4 * E>(static_cast<const float *>(p) + at);
+#pragma unroll
+        for (int k = 0; k < E; ++k) v[k] = __uint_as_float(r.w[k]);
+        return;
+    }
+    const Words<2 * E> r = load_words<2 * E>(static_cast<const uint16_t *>(p) + at);
+#pragma unroll
+    for (int k = 0; k < E; k += 2) {
+        if (dt == TQ_DTYPE_BF16) {
+            v[k] = bf16_lo(r.w[k / 2]);
+            v[k + 1] = bf16_hi(r.w[k / 2]);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r.w[k / 2]));
+            v[k] = f.x;
+            v[k + 1] = f.y;
+        }
+    }
+}
+template <int E>
+__device__ __forceinline__ void store_vec(void * p, int dt, int64_t at, const float * v) {
+    if (dt == TQ_DTYPE_F32) {
+        Words<4 * E> r;
+#pragma unroll
+        for (int k = 0; k < E; ++k) r.w[k] = __float_as_uint(v[k]);
+        store_words<4 * E>(static_cast<float *>(p) + at, r);
+        return;
+    }
+    Words<2 * E> r;
+#pragma unroll
+    for (int k = 0; k < E; k += 2)
+        r.w[k / 2] = dt == TQ_DTYPE_BF16 ? fm::pack2<true>(v[k], v[k + 1]) : fm::pack2<false>(v[k], v[k + 1]);
+    store_words<2 * E>(static_cast<uint16_t *>(p) + at, r);
+}
 __device__ __forceinline__ float signed_by(const uint32_t * bits, int i, float v) {
     return ((bits[i >> 5] >> (i & 31)) & 1u) ? -v : v;
 }
@@ -278,8 +349,9 @@ __global__ void __launch_bounds__(kTpThreads) tree_prep_kernel(const __grid_cons
             v[k] = s;
         }
     } else {
+        load_vec<E>(a.q, a.q_dtype, vec * D + E * lane, v);
 #pragma unroll
-        for (int k = 0; k < E; ++k) v[k] = signed_by(a.d2_bits, E * lane + k, load_el(a.q, a.q_dtype, vec * D + E * lane + k));
+        for (int k = 0; k < E; ++k) v[k] = signed_by(a.d2_bits, E * lane + k, v[k]);
         warp_fwht<E>(v, lane);
 #pragma unroll
         for (int k = 0; k < E; ++k) v[k] = signed_by(a.d1_bits, E * lane + k, v[k]);
@@ -294,9 +366,9 @@ __global__ void __launch_bounds__(kTpThreads) tree_prep_kernel(const __grid_cons
     const float f = __uint_as_float((uint32_t)(127 - e) << 23);
     const int hk = h / a.group, g = h - hk * a.group;
     const int64_t id = (int64_t)q.r0 * a.n_q_heads + (int64_t)hk * q.n * a.group + (int64_t)node * a.group + g;
-    __half * o = a.q_rows + id * D + E * lane;
 #pragma unroll
-    for (int k = 0; k < E; k += 2) *reinterpret_cast<__half2 *>(o + k) = __floats2half2_rn(v[k] * f, v[k + 1] * f);
+    for (int k = 0; k < E; ++k) v[k] *= f;
+    store_vec<E>(a.q_rows, TQ_DTYPE_F16, id * D + E * lane, v);
     if (lane == 0) a.q_mul[id] = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
@@ -958,12 +1030,10 @@ __global__ void __launch_bounds__(kTmThreads) tree_combine_kernel(const __grid_c
         const float fa = ref == -CUDART_INF_F ? 0.0f : fm::ex2(ref - top), fb = fm::ex2(ml.x - top);
         ref = top;
         sum = sum * fa + ml.y * fb;
+        float x[E];
+        load_vec<E>(o, TQ_DTYPE_F32, E * lane, x);
 #pragma unroll
-        for (int k = 0; k < E; k += 2) {
-            const float2 x = *reinterpret_cast<const float2 *>(o + E * lane + k);
-            v[k] = v[k] * fa + x.x * fb;
-            v[k + 1] = v[k + 1] * fa + x.y * fb;
-        }
+        for (int k = 0; k < E; ++k) v[k] = v[k] * fa + x[k] * fb;
     };
     if (tiles > 0) {
         const int64_t n = sharers(a, units);
@@ -997,7 +1067,8 @@ __global__ void __launch_bounds__(kTmThreads) tree_combine_kernel(const __grid_c
         for (int k = 0; k < E; ++k) v[k] = signed_by(a.d1_bits, E * lane + k, v[k]);
         warp_fwht<E>(v, lane);
 #pragma unroll
-        for (int k = 0; k < E; ++k) store_el(a.out, a.q_dtype, vec * D + E * lane + k, signed_by(a.d2_bits, E * lane + k, v[k]));
+        for (int k = 0; k < E; ++k) v[k] = signed_by(a.d2_bits, E * lane + k, v[k]);
+        store_vec<E>(a.out, a.q_dtype, vec * D + E * lane, v);
     }
 }
 
