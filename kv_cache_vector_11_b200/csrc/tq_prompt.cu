@@ -166,6 +166,9 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         *s_redo = 0;
         s_seq[0] = -1;
     }
+    if (warp == 0) tc::tmem_alloc(sbase + (uint32_t)C::OFF_MISC, 512);
+    if (warp == 4 * NQ + 1 && lane < 3)
+        asm volatile("prefetch.tensormap [%0];" :: "l"(lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap) : "memory");
 
     // Which sequence and tile: the tiles of all sequences are counted one sequence
     // after another, a sequence's last tile first (it has the most keys); blocks of
@@ -188,17 +191,25 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         return n;
     };
     int seq = -1, tile = 0;
+    int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
     if (a.batch <= 128) {
         // every warp for itself, without a barrier
         int before = 0;
         for (int b0 = 0; b0 < a.batch && seq < 0; b0 += 32) {
-            const int n = tiles_of(b0 + lane);
-            const int end = before + warp_scan(n);
+            const int b = min(b0 + lane, a.batch - 1);
+            const int r0 = clamp_to(a.cu_q[b], 0, (int)a.total_q), r1 = clamp_to(a.cu_q[b + 1], r0, (int)a.total_q);
+            const int c0 = clamp_to(a.cu_k[b], 0, (int)a.total_k), c1 = clamp_to(a.cu_k[b + 1], c0, (int)a.total_k);
+            const int nt = b0 + lane < a.batch ? (int)((unsigned)(r1 - r0 + cta_queries - 1) / (unsigned)cta_queries) : 0;
+            const int end = before + warp_scan(nt);
             const unsigned hit = __ballot_sync(0xffffffffu, tau < end);
             if (hit != 0u) {
                 const int at = __ffs((int)hit) - 1;
                 seq = b0 + at;
                 tile = __shfl_sync(0xffffffffu, end, at) - 1 - tau;
+                q0 = __shfl_sync(0xffffffffu, r0, at);
+                q1 = __shfl_sync(0xffffffffu, r1, at);
+                k0 = __shfl_sync(0xffffffffu, c0, at);
+                k1 = __shfl_sync(0xffffffffu, c1, at);
             }
             before = __shfl_sync(0xffffffffu, end, 31);
         }
@@ -227,28 +238,29 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         __syncthreads();
         seq = s_seq[0];
         tile = s_seq[1];
+        if (seq >= 0) {
+            q0 = clamp_to(a.cu_q[seq], 0, (int)a.total_q);
+            q1 = clamp_to(a.cu_q[seq + 1], q0, (int)a.total_q);
+            k0 = clamp_to(a.cu_k[seq], 0, (int)a.total_k);
+            k1 = clamp_to(a.cu_k[seq + 1], k0, (int)a.total_k);
+        }
     }
-    if (seq < 0) return;                                  // past the last tile
-    const int q0 = clamp_to(a.cu_q[seq], 0, (int)a.total_q), q1 = clamp_to(a.cu_q[seq + 1], q0, (int)a.total_q);
-    const int k0 = clamp_to(a.cu_k[seq], 0, (int)a.total_k), k1 = clamp_to(a.cu_k[seq + 1], k0, (int)a.total_k);
     const int nq = q1 - q0, nk = k1 - k0;
     const int i0 = tile * cta_queries;                    // first query of this CTA
     const int shift = nk - nq;                            // query i attends the keys below i + shift + 1
     const int i_last = min(i0 + cta_queries, nq) - 1;
     const int n_keys = max(i_last + shift + 1, 0);        // (at most nk)
-    const int n = (n_keys + kTile - 1) / kTile;           // key tiles, taken from the last to the first
+    // key tiles, taken from the last to the first; none past the last row tile
+    const int n = seq < 0 ? 0 : (n_keys + kTile - 1) / kTile;
     const int full_keys = min(max(i0 + shift + 1, 0), nk);    // keys that every row attends
     const int n_edge = n - full_keys / kTile;             // tiles with a key that some row does not attend
     const int slots = NQ == 2 && i0 + a.queries < nq ? 2 : 1;
     const int h0 = hg * a.heads, hk = h0 / (a.n_q_heads / a.n_kv_heads);
 
-    if (n > 0) {
-        if (warp == 0) tc::tmem_alloc(sbase + (uint32_t)C::OFF_MISC, 512);
-        tc::fence_before_sync();
-        __syncthreads();
-        tc::fence_after_sync();
-    }
-    const uint32_t tmem = __shfl_sync(0xffffffffu, n > 0 ? *s_tmem : 0u, 0);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
     const int ctrl = warp - 4 * NQ;                       // 0 and 3: MMAs, 1: copies, 2: value scan
 
     if (n > 0 && ctrl == 1) {
@@ -465,7 +477,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         const int r = tid & 127;
         const int g = r % a.heads, qt = r / a.heads;
         const int qi = i0 + i * a.queries + qt;
-        const bool valid = qt < a.queries && qi < nq;
+        const bool valid = seq >= 0 && qt < a.queries && qi < nq;
         const int lim = valid ? min(max(qi + shift + 1, 0), nk) : 0;      // keys of this row
         T * op = static_cast<T *>(a.out) + ((int64_t)(q0 + qi) * a.n_q_heads + h0 + g) * D;
         if (n > 0 && i < slots) {
@@ -518,18 +530,33 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             if (ok) {
                 tc::fence_after_sync();
                 const float inv = lim > 0 ? 1.0f / st.sum : 0.0f;
+                // The rows go through shared memory (the row tile of the queries, which
+                // nothing reads any more; each warp has its rows' share), so that a
+                // store covers whole rows: row by row from their threads, 16 bytes of 32
+                // rows at a time, they take 5000 cycles, this way EPILOGUE.
+                constexpr int RB = 2 * D, PER = 512 / RB, CH = RB / 16;      // bytes of a row, rows of a store, chunks of a row
+                unsigned char * mine = smem + i * NH * C::BUF + (warp & 3) * (32 * RB);
+#pragma unroll
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     fm::tmem_ld32(o_tm + (uint32_t)c, o);
-                    if (!valid) continue;
 #pragma unroll
                     for (int x = 0; x < 32; x += 8) {
                         uint32_t w[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
                             w[y] = lim > 0 ? fm::pack2<BF16>(__uint_as_float(o[x + 2 * y]) * inv, __uint_as_float(o[x + 2 * y + 1]) * inv) : 0u;
-                        *reinterpret_cast<uint4 *>(op + c + x) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(mine + lane * RB + 16 * (((c + x) >> 3) ^ (lane & 7))) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
+                }
+                __syncwarp();
+                const uint64_t to = valid ? reinterpret_cast<uint64_t>(op) : 0u;
+#pragma unroll 4
+                for (int k = 0; k < 32; k += PER) {
+                    const int row = k + lane / CH, c = lane % CH;
+                    const uint64_t dst = __shfl_sync(0xffffffffu, to, row);
+                    const uint4 w = *reinterpret_cast<const uint4 *>(mine + row * RB + 16 * (c ^ (row & 7)));
+                    if (dst != 0u) *reinterpret_cast<uint4 *>(dst + 16u * (uint32_t)c) = w;
                 }
                 tc::fence_before_sync();
             }
@@ -537,7 +564,6 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4 *>(op + c) = make_uint4(0u, 0u, 0u, 0u);
         }
     }
-    if (n == 0) return;
     __syncthreads();
     tc::fence_after_sync();
     if (*s_err != 0 && tid == 0 && a.status != nullptr) atomicOr(a.status, TQ_STATUS_TIMEOUT);
