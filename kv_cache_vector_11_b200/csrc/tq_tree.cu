@@ -85,11 +85,13 @@ struct TreeArgs {
     int32_t n_ctas;
     // workspace
     int64_t * unit0;            // [batch + 1] units before a request
+    int32_t * row_request;      // [n_rows] the request of a row, -1 for padding
     __half * q_rows;            // [n_rows * n_q_heads][d], by request, KV head, node, head
     float * q_mul;              // what a row's scores are multiplied by
-    float * own;                // [n_rows * n_q_heads * 2][d] partial sums
+    int64_t own_rows;           // n_rows * n_q_heads, up to a multiple of 32
+    float * own;                // partial sums of streams x own_rows rows (part_at)
     float2 * own_ml;            //   their (ref, sum of weights)
-    float * more;               // [n_ctas][2 * 128][d] parts of sets that began in an earlier CTA
+    float * more;               // of n_ctas x 256 rows, parts of sets that began in an earlier CTA
     float2 * more_ml;
 };
 
@@ -113,7 +115,20 @@ __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kT
 // CTA c, and the CTA whose range holds unit u.
 __device__ __forceinline__ int64_t sharers(const TreeArgs & a, int64_t units) { return min((int64_t)a.n_ctas, units); }
 __device__ __forceinline__ int64_t first_unit(int64_t c, int64_t units, int64_t n) { return n > 0 ? units * min(c, n) / n : 0; }
-__device__ __forceinline__ int cta_of(int64_t u, int64_t units, int64_t n) { return (int)(((u + 1) * n - 1) / units); }
+__device__ __forceinline__ int cta_of(int64_t u, int64_t units, int64_t n) {
+    const int64_t x = (u + 1) * n - 1;
+    // (a 32-bit division where it does: the 64-bit one takes some 500 cycles)
+    return x <= 0xFFFFFFFFll ? (int)((uint32_t)x / (uint32_t)units) : (int)(x / units);
+}
+
+// Where column `col` (a multiple of 4) of row `row` of the partial sums lies:
+// 32 rows take turns, four columns each, since a thread has a row and a warp
+// then writes 512 bytes in a piece (row by row, 16 bytes of 32 rows at a time,
+// the accumulators take ROWWISE cycles to write, this way COLWISE).
+template <int D>
+__device__ __forceinline__ int64_t part_at(int64_t row, int col) {
+    return ((row >> 5) * (D / 4) + (col >> 2)) * 128 + (row & 31) * 4;
+}
 
 // The parts of this CTA's range, one per (request, KV head, row set).
 struct Part {
@@ -331,9 +346,12 @@ __global__ void __launch_bounds__(kTpThreads) tree_prep_kernel(const __grid_cons
     const int64_t vec = (int64_t)(blockIdx.x - 1) * NW + warp;
     if (vec >= (int64_t)a.n_rows * a.n_q_heads) return;
     const int row = (int)(vec / a.n_q_heads), h = (int)(vec - (int64_t)row * a.n_q_heads);
-    const Request q = request_of(a, request_of_row(a, row, lane));
+    const int b = request_of_row(a, row, lane);
+    const Request q = request_of(a, b);
     const int node = row - q.r0;
-    if (node < 0 || node >= q.n) return;
+    const bool is_row = node >= 0 && node < q.n;
+    if (h == 0 && lane == 0) a.row_request[row] = is_row ? b : -1;
+    if (!is_row) return;
     float v[E];
     if (a.dense) {
         for (int i = lane; i < D; i += 32) x_s[warp][i] = load_el(a.q, a.q_dtype, vec * D + i);
@@ -907,8 +925,8 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
             const int64_t id = p.row_id + in_set;
             const bool own = p.tile0 == 0;
             const int slot_row = w * kTile + r;
-            float2 * ml = own ? a.own_ml + (MODE == STREAM ? 2 * id + w : id)
-                              : a.more_ml + (int64_t)blockIdx.x * (2 * kTile) + slot_row;
+            const int64_t part_row = own ? (MODE == STREAM ? w * a.own_rows : 0) + id : (int64_t)blockIdx.x * (2 * kTile) + slot_row;
+            float2 * ml = (own ? a.own_ml : a.more_ml) + part_row;
             if (!takes) {
                 if (MODE == STREAM && valid) *ml = make_float2(-CUDART_INF_F, 0.0f);
                 tile0 += p.tiles;
@@ -972,15 +990,14 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
             if (!ok) break;
             tc::fence_after_sync();
             if (warp_valid) {
-                float * dst = own ? a.own + (MODE == STREAM ? 2 * id + w : id) * D
-                                  : a.more + ((int64_t)blockIdx.x * (2 * kTile) + slot_row) * D;
+                float * dst = own ? a.own : a.more;
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     fm::tmem_ld32(o_tm + (uint32_t)c, o);
                     if (valid) {
 #pragma unroll
                         for (int x = 0; x < 32; x += 4)
-                            *reinterpret_cast<uint4 *>(dst + c + x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                            *reinterpret_cast<uint4 *>(dst + part_at<D>(part_row, c + x)) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
                     }
                 }
                 if (valid) *ml = make_float2(st.ref, st.sum);
@@ -997,78 +1014,130 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
 }
 
 // ---------------------------------------------------------------------------
-// Merge and rotation back: one warp per (row, head)
+// Merge and rotation back: 32 rows a CTA
 // ---------------------------------------------------------------------------
 
 constexpr int kTmThreads = 256;
 
+// First a lane has a row and a warp an eighth of the columns, so that the parts
+// are read as they were written (part_at); the sums meet in shared memory, and
+// every warp rotates four rows back.
 template <int D>
 __global__ void __launch_bounds__(kTmThreads) tree_combine_kernel(const __grid_constant__ TreeArgs a) {
-    constexpr int E = D / 32, NW = kTmThreads / 32;
-    __shared__ float y_s[NW][D];
+    constexpr int E = D / 32, NW = kTmThreads / 32, CH = D / 4 / NW, LD = D + 4, RW = 32 / NW;
+    __shared__ __align__(16) float y_s[32][LD];
+    __shared__ int64_t out_s[32];                        // where a row's output starts, -1: no row
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t vec = (int64_t)blockIdx.x * NW + warp;
-    if (vec >= (int64_t)a.n_rows * a.n_q_heads) return;
-    const int row = (int)(vec / a.n_q_heads), h = (int)(vec - (int64_t)row * a.n_q_heads);
-    const int b = request_of_row(a, row, lane);
-    const Request q = request_of(a, b);
-    const int node = row - q.r0;
-    if (node < 0 || node >= q.n) return;
-    const int hk = h / a.group, in_req = node * a.group + h - hk * a.group;
-    const int set = in_req / a.rows_per_set, in_set = in_req - set * a.rows_per_set;
-    const int64_t id = (int64_t)q.r0 * a.n_q_heads + (int64_t)hk * q.n * a.group + in_req;
-    const int tiles = tiles_of(q.len);
+    const int64_t id = (int64_t)blockIdx.x * 32 + lane;
     wait_for_previous();
-    const int64_t units = a.unit0[a.batch];
-    const int64_t u0 = a.unit0[b] + ((int64_t)hk * sets_of(a, q.n) + set) * tiles;
-    float ref = -CUDART_INF_F, sum = 0.0f, v[E];
-#pragma unroll
-    for (int k = 0; k < E; ++k) v[k] = 0.0f;
-    auto add = [&](float2 ml, const float * o) {
-        if (ml.x == -CUDART_INF_F) return;               // no key attended
-        const float top = fmaxf(ref, ml.x);              // (a NaN stays in the sums)
-        const float fa = ref == -CUDART_INF_F ? 0.0f : fm::ex2(ref - top), fb = fm::ex2(ml.x - top);
-        ref = top;
-        sum = sum * fa + ml.y * fb;
-        float x[E];
-        load_vec<E>(o, TQ_DTYPE_F32, E * lane, x);
-#pragma unroll
-        for (int k = 0; k < E; ++k) v[k] = v[k] * fa + x[k] * fb;
-    };
-    if (tiles > 0) {
-        const int64_t n = sharers(a, units);
-        const int c0 = cta_of(u0, units, n), c1 = cta_of(u0 + tiles - 1, units, n);
-        for (int s = 0; s < a.streams; ++s) add(a.own_ml[id * a.streams + s], a.own + (id * a.streams + s) * D);
-        for (int c = c0 + 1; c <= c1; ++c)
-            for (int s = 0; s < a.streams; ++s) {
-                const int64_t at = (int64_t)c * (2 * kTile) + s * kTile + in_set;
-                add(a.more_ml[at], a.more + at * D);
+    // the row: its request, place in the request, and parts
+    int64_t dst = -1, u0 = 0;
+    int tiles = 0, in_set = 0;
+    if (id < (int64_t)a.n_rows * a.n_q_heads) {
+        const int b = a.row_request[(uint32_t)id / (uint32_t)a.n_q_heads];
+        if (b >= 0) {
+            const Request q = request_of(a, b);
+            const int rem = (int)id - q.r0 * a.n_q_heads;    // (rows times heads fit 30 bits)
+            if (rem >= 0 && rem < q.n * a.n_q_heads) {
+                const int per = q.n * a.group, hk = rem / per, in_req = rem - hk * per;
+                const int node = in_req / a.group, set = in_req / a.rows_per_set;
+                in_set = in_req - set * a.rows_per_set;
+                tiles = tiles_of(q.len);
+                u0 = a.unit0[b] + ((int64_t)hk * sets_of(a, q.n) + set) * tiles;
+                dst = ((int64_t)(q.r0 + node) * a.n_q_heads + hk * a.group + in_req - node * a.group) * D;
             }
+        }
+    }
+    if (warp == 0) out_s[lane] = dst;
+    const int64_t units = a.unit0[a.batch], n = sharers(a, units);
+    int c0 = 0, c1 = -1;                                 // the CTAs that share the row's tiles
+    if (tiles > 0) {
+        c0 = cta_of(u0, units, n);
+        c1 = cta_of(u0 + tiles - 1, units, n);
+    }
+    // its parts, U at a time: their reads do not wait for one another
+    constexpr int U = D == 256 ? 2 : 4;
+    const int n_parts = (c1 - c0 + 1) * a.streams;
+    float ref = -CUDART_INF_F, sum = 0.0f;
+    float4 acc[CH];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int p0 = 0; p0 < n_parts; p0 += U) {
+        float2 ml[U];
+        float4 x[U][CH];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            ml[u] = make_float2(-CUDART_INF_F, 0.0f);
+            if (p0 + u < n_parts) {
+                const int at_c = a.streams == 2 ? (p0 + u) >> 1 : p0 + u, s = a.streams == 2 ? (p0 + u) & 1 : 0;
+                const int64_t at = at_c == 0 ? s * a.own_rows + id : (int64_t)(c0 + at_c) * (2 * kTile) + s * kTile + in_set;
+                const float * parts = at_c == 0 ? a.own : a.more;
+                ml[u] = (at_c == 0 ? a.own_ml : a.more_ml)[at];
+#pragma unroll
+                for (int k = 0; k < CH; ++k) x[u][k] = *reinterpret_cast<const float4 *>(parts + part_at<D>(at, 4 * (k * NW + warp)));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (ml[u].x == -CUDART_INF_F) continue;      // no key attended (what its part holds is not read)
+            const float top = fmaxf(ref, ml[u].x);       // (a NaN stays in the sums)
+            const float fa = ref == -CUDART_INF_F ? 0.0f : fm::ex2(ref - top), fb = fm::ex2(ml[u].x - top);
+            ref = top;
+            sum = sum * fa + ml[u].y * fb;
+#pragma unroll
+            for (int k = 0; k < CH; ++k) {
+                acc[k].x = acc[k].x * fa + x[u][k].x * fb;
+                acc[k].y = acc[k].y * fa + x[u][k].y * fb;
+                acc[k].z = acc[k].z * fa + x[u][k].z * fb;
+                acc[k].w = acc[k].w * fa + x[u][k].w * fb;
+            }
+        }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a node that attends nothing: zeros
 #pragma unroll
-    for (int k = 0; k < E; ++k) v[k] *= inv;
+    for (int k = 0; k < CH; ++k) acc[k] = make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv);
+    // (a row marked by a NaN sum is NaN whatever its parts hold)
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+        if (isnan(sum)) acc[k] = make_float4(sum, sum, sum, sum);
+        *reinterpret_cast<float4 *>(&y_s[lane][4 * (k * NW + warp)]) = acc[k];
+    }
+    __syncthreads();
     if (a.dense) {
+        float x[RW][E];
 #pragma unroll
-        for (int k = 0; k < E; ++k) y_s[warp][E * lane + k] = v[k];
-        __syncwarp();
-        float x[E];
+        for (int r = 0; r < RW; ++r)
 #pragma unroll
-        for (int k = 0; k < E; ++k) x[k] = 0.0f;
+            for (int k = 0; k < E; ++k) x[r][k] = 0.0f;
         for (int e = 0; e < D; ++e) {
-            const float y = y_s[warp][e];
+            float y[RW];
 #pragma unroll
-            for (int k = 0; k < E; ++k) x[k] = fmaf(__ldg(a.rot_f32 + (int64_t)e * D + 32 * k + lane), y, x[k]);
+            for (int r = 0; r < RW; ++r) y[r] = y_s[RW * warp + r][e];
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                const float w = __ldg(a.rot_f32 + (int64_t)e * D + 32 * k + lane);
+#pragma unroll
+                for (int r = 0; r < RW; ++r) x[r][k] = fmaf(w, y[r], x[r][k]);
+            }
         }
 #pragma unroll
-        for (int k = 0; k < E; ++k) store_el(a.out, a.q_dtype, vec * D + 32 * k + lane, x[k]);
+        for (int r = 0; r < RW; ++r)
+            if (out_s[RW * warp + r] >= 0)
+#pragma unroll
+                for (int k = 0; k < E; ++k) store_el(a.out, a.q_dtype, out_s[RW * warp + r] + 32 * k + lane, x[r][k]);
     } else {
 #pragma unroll
-        for (int k = 0; k < E; ++k) v[k] = signed_by(a.d1_bits, E * lane + k, v[k]);
-        warp_fwht<E>(v, lane);
+        for (int r = 0; r < RW; ++r) {
+            const int64_t to = out_s[RW * warp + r];
+            if (to < 0) continue;
+            float v[E];
 #pragma unroll
-        for (int k = 0; k < E; ++k) v[k] = signed_by(a.d2_bits, E * lane + k, v[k]);
-        store_vec<E>(a.out, a.q_dtype, vec * D + E * lane, v);
+            for (int k = 0; k < E; ++k) v[k] = signed_by(a.d1_bits, E * lane + k, y_s[RW * warp + r][E * lane + k]);
+            warp_fwht<E>(v, lane);
+#pragma unroll
+            for (int k = 0; k < E; ++k) v[k] = signed_by(a.d2_bits, E * lane + k, v[k]);
+            store_vec<E>(a.out, a.q_dtype, to + E * lane, v);
+        }
     }
 }
 
@@ -1110,14 +1179,16 @@ int launch_tree(TreeArgs & a, cudaStream_t st) {
     if constexpr (D == 256) e = launch_tree_main<D, WIDE>(a, st);
     else e = a.streams == 2 ? launch_tree_main<D, STREAM>(a, st) : launch_tree_main<D, PAIR>(a, st);
     if (e) return e;
-    return launch_dependent(tree_combine_kernel<D>, vecs, kTmThreads, 0, st, a);
+    return launch_dependent(tree_combine_kernel<D>, (unsigned)(a.own_rows / 32), kTmThreads, 0, st, a);
 }
+
+int64_t own_rows_of(int64_t vecs) { return (vecs + 31) / 32 * 32; }
 
 // Workspace sections, each from a 256-byte boundary.
 struct TreeSpace {
-    size_t unit0, q_rows, q_mul, own, own_ml, more, more_ml, total;
+    size_t unit0, row_request, q_rows, q_mul, own, own_ml, more, more_ml, total;
 };
-TreeSpace tree_space(int64_t batch, int64_t vecs, int d, int n_ctas) {
+TreeSpace tree_space(int64_t batch, int64_t n_rows, int64_t vecs, int d, int n_ctas) {
     TreeSpace s;
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -1126,10 +1197,11 @@ TreeSpace tree_space(int64_t batch, int64_t vecs, int d, int n_ctas) {
         return here;
     };
     s.unit0 = take((size_t)(batch + 1) * 8);
+    s.row_request = take((size_t)n_rows * 4);
     s.q_rows = take((size_t)vecs * d * 2);
     s.q_mul = take((size_t)vecs * 4);
-    s.own = take((size_t)vecs * 2 * d * 4);
-    s.own_ml = take((size_t)vecs * 2 * 8);
+    s.own = take((size_t)own_rows_of(vecs) * 2 * d * 4);
+    s.own_ml = take((size_t)own_rows_of(vecs) * 2 * 8);
     s.more = take((size_t)n_ctas * 2 * kTile * d * 4);
     s.more_ml = take((size_t)n_ctas * 2 * kTile * 8);
     s.total = at;
@@ -1168,7 +1240,7 @@ extern "C" size_t tq_tree_workspace_size(int32_t batch, int32_t n_rows, int32_t 
                                          int32_t n_kv_heads, int64_t max_len, int32_t head_dim) {
     const char * why;
     if (!tree_sizes_ok(batch, n_rows, max_nodes, n_q_heads, n_kv_heads, max_len, head_dim, &why)) return 0;
-    return tree_space(batch, (int64_t)n_rows * n_q_heads, head_dim, device_sm_count()).total;
+    return tree_space(batch, n_rows, (int64_t)n_rows * n_q_heads, head_dim, device_sm_count()).total;
 }
 
 extern "C" tq_status tq_tree_attention(const tq_rotation * rot, int32_t k_bits, int32_t v_bits, int32_t block,
@@ -1254,10 +1326,12 @@ extern "C" tq_status tq_tree_attention(const tq_rotation * rot, int32_t k_bits, 
     a.streams = head_dim < 256 && (int64_t)max_nodes * a.group <= kTile ? 2 : 1;
     a.rows_per_set = head_dim < 256 && a.streams == 1 ? 2 * kTile : kTile;
     unsigned char * ws = static_cast<unsigned char *>(workspace);
-    const TreeSpace sp = tree_space(batch, (int64_t)n_rows * n_q_heads, head_dim, a.n_ctas);
+    const TreeSpace sp = tree_space(batch, n_rows, (int64_t)n_rows * n_q_heads, head_dim, a.n_ctas);
     a.unit0 = reinterpret_cast<int64_t *>(ws + sp.unit0);
+    a.row_request = reinterpret_cast<int32_t *>(ws + sp.row_request);
     a.q_rows = reinterpret_cast<__half *>(ws + sp.q_rows);
     a.q_mul = reinterpret_cast<float *>(ws + sp.q_mul);
+    a.own_rows = own_rows_of((int64_t)n_rows * n_q_heads);
     a.own = reinterpret_cast<float *>(ws + sp.own);
     a.own_ml = reinterpret_cast<float2 *>(ws + sp.own_ml);
     a.more = reinterpret_cast<float *>(ws + sp.more);
