@@ -639,8 +639,8 @@ extern "C" tq_status tq_prompt_attention(const void * q, const void * k, const v
     if (n_q_heads > 65535) return fail(TQ_ERR_UNSUPPORTED, "more than 65535 query heads");
     if (batch < 1 || total_q < 0 || total_k < 0)
         return fail(TQ_ERR_INVALID_ARG, "batch must be >= 1, total_q and total_k >= 0");
-    if (total_q > INT32_MAX || total_k > INT32_MAX)
-        return fail(TQ_ERR_UNSUPPORTED, "more than 2^31 - 1 packed tokens");
+    if (total_q > INT32_MAX - 255 || total_k > INT32_MAX - 255)
+        return fail(TQ_ERR_UNSUPPORTED, "more than 2^31 - 256 packed tokens");
     if (std::isnan(scale) || std::isinf(scale)) return fail(TQ_ERR_INVALID_ARG, "scale is not finite");
     if (q_stride < (int64_t)n_q_heads * head_dim || k_stride < (int64_t)n_kv_heads * head_dim ||
         v_stride < (int64_t)n_kv_heads * head_dim || ((q_stride | k_stride | v_stride) & 7) != 0)

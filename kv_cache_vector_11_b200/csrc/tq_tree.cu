@@ -1227,7 +1227,7 @@ bool tree_sizes_ok(int32_t batch, int32_t n_rows, int32_t max_nodes, int32_t n_q
     else if (n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads != 0)
         *why = "n_q_heads must be a positive multiple of n_kv_heads";
     else if ((int64_t)n_rows * n_q_heads > INT32_MAX / 2) *why = "more than 2^30 rows times heads";
-    else if (max_len > INT32_MAX) *why = "max_len above 2^31 - 1";
+    else if (max_len > INT32_MAX - 255) *why = "max_len above 2^31 - 256";
     return *why == nullptr;
 }
 

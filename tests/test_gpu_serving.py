@@ -279,6 +279,60 @@ def test_prompt_graph_stream_and_lengths_of_the_replay(tq):
     assert torch.equal(replay[:290], tq.prompt_attention(q, k, v, cu)[:290])
 
 
+@pytest.mark.parametrize("batch", [33, 128, 129, 400, 900])
+def test_prompt_many_sequences(tq, batch):
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(0, 9, batch).tolist()
+    lens[batch // 2] = 300
+    _prompt(tq, lens, lens, 2, 1, 64, "bf16", pad=4)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prompt_runs_agree_bit_for_bit(tq, d):
+    """Every wait of the kernel names a phase of its barrier by parity only; a wait
+    that answers a phase too early shows as an output that changes from run to run
+    (with other work in between, so that the timing changes)."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    for lens, hq, hk in (([1500], 2, 1), ([1, 127, 0, 128, 129, 2, 300], 3, 1), ([700, 40], 2, 2)):
+        n = sum(lens)
+        q, k, v = (torch.randn((n, h, d), generator=g, device="cuda").bfloat16() for h in (hq, hk, hk))
+        cu = i32(np.cumsum([0] + lens))
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        first = tq.prompt_attention(q, k, v, cu, status=status)
+        for _ in range(25):
+            torch.randn(1 << 20, device="cuda")
+            assert torch.equal(tq.prompt_attention(q, k, v, cu, status=status), first)
+        assert int(status) == 0
+
+
+def test_prompt_and_tree_on_two_streams_at_once(tq):
+    rng = np.random.default_rng(11)
+    d, page = 128, 32
+    table, n_pages = S.page_tables_for(rng, [2000, 700], page)
+    pages = S.cache_to(S.random_cache(rng, n_pages, 2, page, d, 4, 3), "cuda")
+    rot = tq.Rotation("wht", d, d, W.SEED_ROT)
+    kc, vc = tq.build_codebook(4)[0], tq.build_codebook(3)[0]
+    q, k = (torch.randn((900, h, d), device="cuda").bfloat16() for h in (8, 2))
+    cu_p, cu_t, lens, tab = i32([0, 800, 900]), i32([0, 40, 60]), i32([2000, 700]), i32(table)
+
+    def tree(ws, stream=None):
+        return tq.tree_attention(rot, 4, 3, kc, vc, q[:60], cu_t, lens, pages, tab, page, 40, 2000, workspace=ws, stream=stream)
+    need = tq.tree_workspace_size(2, 60, 40, 8, 2, 2000, d)
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    want_p, want_t = tq.prompt_attention(q, k, k, cu_p), tree(ws[0])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        with torch.cuda.stream(streams[0]):
+            got.append((tq.prompt_attention(q, k, k, cu_p), want_p))
+        for i in (0, 1):
+            with torch.cuda.stream(streams[1 + i]):
+                got.append((tree(ws[i]), want_t))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in got)
+
+
 # -- drafted tokens over the cache ------------------------------------------------------------
 
 def _tree(tq, nodes, lens, hq, hk, d, kb, vb, page, dtype="bf16", kind="wht", chain=False, seed=0, masks=None, scale=0.0,
@@ -373,6 +427,42 @@ def test_tree_many_requests(tq):
     rng = np.random.default_rng(1)
     lens = rng.integers(1, 400, 150).tolist()
     _tree(tq, [1] * 150, lens, 2, 2, 64, 4, 4, 32, chain=True)
+
+
+def test_tree_more_requests_than_a_search_step(tq):
+    rng = np.random.default_rng(5)
+    nodes = rng.integers(0, 3, 1100).tolist()
+    lens = [int(x) + n for x, n in zip(rng.integers(0, 40, 1100), nodes)]
+    _tree(tq, nodes, lens, 2, 1, 64, 3, 2, 16, chain=True, pad=2)
+
+
+@pytest.mark.parametrize("d,hq,hk,nodes", [(128, 8, 2, [40, 3, 64, 1, 33]), (64, 16, 1, [17, 8, 9, 256, 1]), (256, 4, 1, [70, 2, 32, 33, 1])])
+def test_tree_row_tiles_of_every_filling(tq, d, hq, hk, nodes):
+    # requests with one, two and more row tiles side by side, some of one row
+    lens = [n + x for n, x in zip(nodes, (500, 0, 130, 64, 1000))]
+    _tree(tq, nodes, lens, hq, hk, d, 4, 3, 32)
+
+
+@pytest.mark.parametrize("bits", [2, 3, 4])
+def test_tree_any_ascending_centroids(tq, bits):
+    """The library's codebooks are symmetric; the call asks for ascending ones only."""
+    rng = np.random.default_rng(bits)
+    d, page, n = 128, 16, 90
+    c = np.sort(rng.uniform(-0.5, 0.6, 1 << bits)).astype(np.float16).astype(np.float32)
+    table, n_pages = S.page_tables_for(rng, [n], page)
+    pages = S.random_cache(rng, n_pages, 1, page, d, bits, bits)
+    q = torch.randn((3, 4, d), device="cuda").half()
+    rot = tq.Rotation("wht", d, d, W.SEED_ROT)
+    out = tq.tree_attention(rot, bits, bits, c, c, q, i32([0, 3]), i32([n]), S.cache_to(pages, "cuda"), i32(table), page, 3, n)
+    ref, absum, sq = osv.tree_attention(f64(q), P.oracle_rotation("wht", d, W.SEED_ROT), [0, 3], [n], None, pages, table, page,
+                                        c, c, bits, bits)
+    assert np.all(np.linalg.norm(f64(out) - ref, axis=-1) <= S.tree_bound(ref, absum, sq, "f16", d, n))
+
+
+@pytest.mark.parametrize("amp", [1e-12, 1e12])
+def test_tree_query_magnitudes(tq, amp):
+    """Rows of any fp32 magnitude: the products see them scaled to one."""
+    _tree(tq, [5], [150], 4, 2, 128, 4, 3, 16, dtype="f32", amp=amp, scale=0.1 / amp, l2=False)
 
 
 def test_tree_masks_that_leave_rows_empty(tq):
@@ -481,6 +571,28 @@ def test_tree_captured_twice_and_replayed(tq):
         torch.cuda.synchronize()
         want = call()
         assert torch.equal(outs[0], want) and torch.equal(outs[1], want), new
+
+
+@pytest.mark.parametrize("d,hq", [(128, 8), (128, 4), (256, 8), (64, 8)])
+def test_tree_runs_agree_bit_for_bit(tq, d, hq):
+    rng = np.random.default_rng(d + hq)
+    page, nodes, lens = 64, [30, 1, 64], [3000, 129, 900]
+    table, n_pages = S.page_tables_for(rng, lens, page)
+    pages = S.cache_to(S.random_cache(rng, n_pages, 2, page, d, 4, 3), "cuda")
+    kc, vc = tq.build_codebook(4)[0], tq.build_codebook(3)[0]
+    rot = tq.Rotation("wht", d, d, W.SEED_ROT)
+    q = torch.randn((95, hq, d), device="cuda").bfloat16()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(tq.tree_workspace_size(3, 95, 64, hq, 2, 3000, d), dtype=torch.uint8, device="cuda")
+
+    def call():
+        return tq.tree_attention(rot, 4, 3, kc, vc, q, i32([0, 30, 31, 95]), i32(lens), pages, i32(table), page, 64, 3000,
+                                 workspace=ws, status=status)
+    first = call()
+    for _ in range(25):
+        torch.randn(1 << 20, device="cuda")
+        assert torch.equal(call(), first)
+    assert int(status) == 0
 
 
 def test_tree_is_deterministic(tq):

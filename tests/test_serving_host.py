@@ -71,6 +71,8 @@ def prompt(q=FAKE, k=FAKE, v=FAKE, dtype=1, cu_q=FAKE, cu_k=None, batch=2, tq_=8
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(out=None), INVALID), (dict(cu_q=None), INVALID),
     (dict(q=FAKE + 8), INVALID), (dict(out=FAKE + 8), INVALID), (dict(cu_k=FAKE + 2), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(tq_=0, q=None), OK),
+    (dict(tq_=2**31 - 200), UNSUPPORTED), (dict(tk=2**31 - 200, cu_k=FAKE), UNSUPPORTED),
+    (dict(batch=2**31 - 1, hq=4, hk=4, ks=512, vs=512), UNSUPPORTED),
 ])
 def test_prompt_refusals(kw, code):
     assert prompt(**kw) == code
@@ -94,7 +96,8 @@ def tree(rot, kb=4, vb=3, block=32, q=FAKE, dtype=1, cu=FAKE, batch=2, rows=8, n
     (dict(kc=None), INVALID), (dict(vn=None), INVALID), (dict(out=None), INVALID), (dict(ws=None), INVALID),
     (dict(ws_bytes=0), INVALID), (dict(ws=FAKE + 128), INVALID), (dict(q=FAKE + 8), INVALID),
     (dict(vc=FAKE + 4), INVALID), (dict(mask=FAKE + 4), INVALID), (dict(scale=float("nan")), INVALID),
-    (dict(rows=0, q=None), OK),
+    (dict(rows=0, q=None), OK), (dict(max_len=2**31 - 200, max_pages=2**30), INVALID),
+    (dict(n_pages=2**16, hk=1, page=65536), UNSUPPORTED), (dict(n_pages=2**31 - 1, hk=4, hq=4), UNSUPPORTED),
 ])
 def test_tree_refusals(rot, kw, code):
     assert tree(rot, **kw) == code
