@@ -52,6 +52,7 @@ namespace {
 using fm::kTile;
 
 constexpr int kTaMaxNodes = 256;
+constexpr int kFewRows = 8;          // rows that share a key tile in tree_few_kernel
 
 enum TreeMode { PAIR = 0, STREAM = 1, WIDE = 2 };
 
@@ -82,7 +83,8 @@ struct TreeArgs {
     uint32_t * status;
     int32_t rows_per_set;       // rows that share a CTA: 256 (PAIR) or 128
     int32_t streams;            // own slots of a row: 2 (STREAM) or 1
-    int32_t n_ctas;
+    int32_t n_ctas;             // sharers of the units: CTAs, or warps where few rows share a tile
+    int32_t more_rows;          // rows of a sharer in `more`: 256, or 8
     // workspace
     int64_t * unit0;            // [batch + 1] units before a request
     int32_t * row_request;      // [n_rows] the request of a row, -1 for padding
@@ -91,7 +93,7 @@ struct TreeArgs {
     int64_t own_rows;           // n_rows * n_q_heads, up to a multiple of 32
     float * own;                // partial sums of streams x own_rows rows (part_at)
     float2 * own_ml;            //   their (ref, sum of weights)
-    float * more;               // of n_ctas x 256 rows, parts of sets that began in an earlier CTA
+    float * more;               // of n_ctas x more_rows rows, parts of sets that began with an earlier sharer
     float2 * more_ml;
 };
 
@@ -925,7 +927,7 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
             const int64_t id = p.row_id + in_set;
             const bool own = p.tile0 == 0;
             const int slot_row = w * kTile + r;
-            const int64_t part_row = own ? (MODE == STREAM ? w * a.own_rows : 0) + id : (int64_t)blockIdx.x * (2 * kTile) + slot_row;
+            const int64_t part_row = own ? (MODE == STREAM ? w * a.own_rows : 0) + id : (int64_t)blockIdx.x * a.more_rows + slot_row;
             float2 * ml = (own ? a.own_ml : a.more_ml) + part_row;
             if (!takes) {
                 if (MODE == STREAM && valid) *ml = make_float2(-CUDART_INF_F, 0.0f);
@@ -1014,21 +1016,365 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
 }
 
 // ---------------------------------------------------------------------------
-// Merge and rotation back: 32 rows a CTA
+// Few rows: at most 8 rows share a key tile (single tokens, small groups)
+// ---------------------------------------------------------------------------
+
+// A tile of 128 rows would be nearly empty, and its unpacking into shared memory
+// the whole cost.  Here every warp streams 16 tokens at a time for itself and
+// unpacks them into the registers of m16n8k16 MMAs, which hold the tokens (or
+// the output coordinates) in their 16 rows and the query rows in their 8 columns:
+//
+//   scores: A = 16 tokens x 16 coordinates of keys, lane 4 g + t with tokens g,
+//     g + 8 and the coordinates t D/4 .. (t + 1) D/4 - 1, a run of the packed row;
+//   values: A = 16 coordinates x 16 tokens, lane 4 g + t with the coordinates
+//     4 g .. 4 g + 3 of each block and the tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9;
+//     B = the weights, transposed by movmatrix.
+//
+// Pairs of codes become pairs of fp16 centroids by one shared-memory lookup (a
+// copy of the table per lane, so no two lanes meet in a bank), times the norm.
+// The units are shared among the warps of the grid as they are among its CTAs
+// elsewhere.  FEWTIME
+template <int D>
+struct FewCfg {
+    static constexpr int NB = D / 32, SEG = D / 4;       // blocks; coordinates of a lane's run of keys
+    static constexpr int WARPS = D == 256 ? 8 : 16;
+    static constexpr int STAGES = 3;
+    static constexpr int SLAB = 16 * (2 * D / 2 + 4 * NB);   // packed bytes of 16 tokens at 4 bits: codes, norms
+    static constexpr int OFF_VC = 16 * D / 2, OFF_KN = 2 * OFF_VC, OFF_VN = OFF_KN + 32 * NB;
+    static constexpr int OFF_RING = 2 * 256 * 128;       // behind the two tables
+    static constexpr int SMEM = OFF_RING + WARPS * STAGES * SLAB;
+    static_assert(SMEM <= 232448, "shared memory of a CTA");
+};
+
+__device__ __forceinline__ void mma_16816(float * d, const uint32_t * a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t table_at(uint32_t addr) {
+    uint32_t v;
+    asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));      // (written before the first unit only)
+    return v;
+}
+
+// Scores of 16 tokens: acc += keys x queries.  `codes`: the slab's packed keys,
+// qf: the lane's query words (B fragments in order), tab: the lane's copy.
+template <int D, int BITS>
+__device__ __forceinline__ void few_scores(float * acc, const unsigned char * codes, const __half * norms, const uint32_t * qf,
+                                           uint32_t tab, int g, int t) {
+    constexpr int NB = D / 32, SEG = D / 4, ROW = D / 8 * BITS;
+    constexpr int PIECE = SEG < 32 ? SEG : 32;           // codes taken at a time: a block, or half of one
+    constexpr uint32_t MASK = (1u << (2 * BITS)) - 1u;
+#pragma unroll
+    for (int b = 0; b < SEG / PIECE; ++b) {
+        const int blk = D == 64 ? t >> 1 : t * (SEG / 32) + b;
+        uint32_t w[2][BITS + 1];
+        __half2 norm[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const uint32_t * row = reinterpret_cast<const uint32_t *>(codes + (g + 8 * r) * ROW) + blk * BITS;
+#pragma unroll
+            for (int i = 0; i < BITS; ++i) w[r][i] = row[i];
+            w[r][BITS] = 0u;
+            if (D == 64 && (t & 1)) {                     // the second half of the block
+#pragma unroll
+                for (int i = 0; i < BITS; ++i) {
+                    const int lo = i + BITS / 2;
+                    w[r][i] = lo < BITS ? (BITS % 2 ? __funnelshift_r(w[r][lo], w[r][lo + 1 <= BITS ? lo + 1 : BITS], 16) : w[r][lo]) : 0u;
+                }
+            }
+            norm[r] = __half2half2(norms[(g + 8 * r) * NB + blk]);
+        }
+#pragma unroll
+        for (int k = 0; k < PIECE / 4; ++k) {             // 4 codes of each token: one MMA
+            uint32_t a[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int bit = 2 * BITS * (2 * k + h), wi = bit >> 5, sh = bit & 31;
+                    const uint32_t x = sh + 2 * BITS <= 32 ? w[r][wi] >> sh : __funnelshift_r(w[r][wi], w[r][wi + 1], sh);
+                    a[2 * h + r] = hmul2_u(table_at(tab + (x & MASK) * 128u), norm[r]);
+                }
+            mma_16816(acc, a, qf[2 * (b * (PIECE / 4) + k)], qf[2 * (b * (PIECE / 4) + k) + 1]);
+        }
+    }
+}
+
+// Output of 16 tokens: o += values x weights (b0, b1: the lane's weights).
+template <int D, int BITS>
+__device__ __forceinline__ void few_values(float (*o)[4], const unsigned char * codes, const __half * norms, uint32_t b0, uint32_t b1,
+                                           uint32_t tab, int g, int t) {
+    constexpr int NB = D / 32, ROW = D / 8 * BITS;
+    constexpr uint32_t MASK = (1u << (2 * BITS)) - 1u;
+    const int bit = 4 * BITS * g, wi = bit >> 5, sh = bit & 31;       // the lane's 4 codes of a block
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+        uint32_t lo[4], hi[4];                            // (coordinate 0, 1) and (2, 3) of the four tokens
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int tok = 2 * t + (k & 1) + 8 * (k >> 1);
+            const uint32_t * row = reinterpret_cast<const uint32_t *>(codes + tok * ROW) + blk * BITS;
+            uint32_t x = row[wi];
+            if (BITS == 3) x = __funnelshift_r(x, row[min(wi + 1, 2)], sh);
+            else x >>= sh;
+            lo[k] = table_at(tab + (x & MASK) * 128u);
+            hi[k] = table_at(tab + ((x >> (2 * BITS)) & MASK) * 128u);
+        }
+        uint32_t a0[4], a1[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {                     // tokens 2 t, 2 t + 1; then those 8 on
+            const int tok = 2 * t + 8 * h;
+            const __half2 norm = __halves2half2(norms[tok * NB + blk], norms[(tok + 1) * NB + blk]);
+            a0[2 * h] = hmul2_u(__byte_perm(lo[2 * h], lo[2 * h + 1], 0x5410), norm);
+            a0[2 * h + 1] = hmul2_u(__byte_perm(lo[2 * h], lo[2 * h + 1], 0x7632), norm);
+            a1[2 * h] = hmul2_u(__byte_perm(hi[2 * h], hi[2 * h + 1], 0x5410), norm);
+            a1[2 * h + 1] = hmul2_u(__byte_perm(hi[2 * h], hi[2 * h + 1], 0x7632), norm);
+        }
+        mma_16816(o[2 * blk], a0, b0, b1);
+        mma_16816(o[2 * blk + 1], a1, b0, b1);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * FewCfg<D>::WARPS, 1) tree_few_kernel(const __grid_constant__ TreeArgs a) {
+    using C = FewCfg<D>;
+    constexpr int NB = C::NB;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    let_next_start();
+    // the pair tables
+    for (int i = threadIdx.x; i < 2 * 256 * 32; i += 32 * C::WARPS) {
+        const bool v = i >= 256 * 32;
+        const int e = (i >> 5) & 255, bits = v ? a.v_bits : a.k_bits;
+        const uint32_t * tab = v ? a.v_table : a.k_table;
+        auto entry = [&](int c) {
+            return ((tab[c >> 2] >> (8 * (c & 3))) & 0xFFu) | ((tab[4 + (c >> 2)] >> (8 * (c & 3))) & 0xFFu) << 8;
+        };
+        reinterpret_cast<uint32_t *>(smem)[i] = entry(e & ((1 << bits) - 1)) | entry((e >> bits) & ((1 << bits) - 1)) << 16;
+    }
+    wait_for_previous();
+    __syncthreads();
+    const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(smem);
+    const uint32_t k_tab = sbase + 4u * (uint32_t)lane, v_tab = k_tab + 256u * 128u;
+    const uint32_t ring = (uint32_t)(C::OFF_RING + warp * C::STAGES * C::SLAB);
+
+    // this warp's units
+    const int64_t units = a.unit0[a.batch], n = sharers(a, units);
+    const int worker = blockIdx.x * C::WARPS + warp;
+    PartIter it;
+    it.u = first_unit(worker, units, n);
+    it.end = first_unit(worker + 1, units, n);
+    if (it.u >= it.end) return;
+    {
+        // the request of the first one
+        int lo = 0, len = a.batch;
+        while (len > 1) {
+            const int step = (len + 31) >> 5, at = lo + lane * step;
+            const unsigned before = __ballot_sync(0xffffffffu, lane * step < len && a.unit0[min(at, a.batch)] <= it.u);
+            const int k = max(__popc(before) - 1, 0) * step;
+            lo += k;
+            len = min(step, len - k);
+        }
+        it.b = lo;
+    }
+    Part p;
+    while (it.next(a, p)) {
+        const int t0 = p.tile0 * kTile, n_slabs = (min(p.rq.len - t0, p.tiles * kTile) + 15) >> 4;
+        const int ctx0 = p.rq.len - p.rq.n;
+        // 16 tokens lie in one page, one behind the other; the page of the slab to
+        // be fetched next was read a slab earlier
+        int page = 0;
+        auto read_page = [&](int s) {
+            if (s < n_slabs) page = __ldg(a.table + (int64_t)p.b * a.max_pages + ((t0 + 16 * s) >> a.page_shift));
+        };
+        auto fetch = [&](int s) {
+            if (s < n_slabs) {
+                const uint32_t pg = (uint32_t)min(max(page, 0), a.n_pages - 1);
+                const uint64_t row = ((pg * (uint32_t)a.n_kv_heads + (uint32_t)p.hk) << a.page_shift) +
+                                     ((uint32_t)(t0 + 16 * s) & ((1u << a.page_shift) - 1u));
+                const uint32_t dst = sbase + ring + (uint32_t)((s % C::STAGES) * C::SLAB);
+                const int kb = 2 * D * a.k_bits, vb = 2 * D * a.v_bits;          // bytes of codes
+                const unsigned char * kc = reinterpret_cast<const unsigned char *>(a.k_codes) + row * (uint32_t)(D / 8 * a.k_bits);
+                const unsigned char * vc = reinterpret_cast<const unsigned char *>(a.v_codes) + row * (uint32_t)(D / 8 * a.v_bits);
+#pragma unroll
+                for (int i = 0; i < (8 * D + 511) / 512; ++i) {
+                    const int at = 512 * i + 16 * lane;
+                    if (at < kb) tc::cp_async16(dst + (uint32_t)at, kc + at);
+                    if (at < vb) tc::cp_async16(dst + (uint32_t)(C::OFF_VC + at), vc + at);
+                }
+                if (lane < 2 * NB) {
+                    tc::cp_async16(dst + (uint32_t)(C::OFF_KN + 16 * lane), reinterpret_cast<const unsigned char *>(a.k_norms + row * NB) + 16 * lane);
+                    tc::cp_async16(dst + (uint32_t)(C::OFF_VN + 16 * lane), reinterpret_cast<const unsigned char *>(a.v_norms + row * NB) + 16 * lane);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        for (int s = 0; s < C::STAGES; ++s) {
+            read_page(s);
+            fetch(s);
+        }
+        read_page(C::STAGES);
+
+        // queries: row g, the lane's run of coordinates
+        uint32_t qf[D / 8];
+        if (g < p.rows) {
+            const uint4 * q = reinterpret_cast<const uint4 *>(a.q_rows + (p.row_id + g) * D + t * C::SEG);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint4 u = q[i];
+                qf[4 * i] = u.x; qf[4 * i + 1] = u.y; qf[4 * i + 2] = u.z; qf[4 * i + 3] = u.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) qf[i] = 0u;
+        }
+        // this lane's columns of the scores and of the output: rows 2 t and 2 t + 1
+        float mul[2], ref[2] = {-CUDART_INF_F, -CUDART_INF_F}, sum[2] = {0.0f, 0.0f};
+        int node[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int r = 2 * t + c;
+            mul[c] = r < p.rows ? a.q_mul[p.row_id + r] : 0.0f;
+            node[c] = (p.set * a.rows_per_set + min(r, p.rows - 1)) / a.group;
+        }
+        float o[2 * NB][4];
+#pragma unroll
+        for (int i = 0; i < 2 * NB; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[i][k] = 0.0f;
+
+        for (int s = 0; s < n_slabs; ++s) {
+            asm volatile("cp.async.wait_group %0;" :: "n"(C::STAGES - 1) : "memory");
+            __syncwarp();
+            unsigned char * slab = smem + ring + (s % C::STAGES) * C::SLAB;
+            const __half * kn = reinterpret_cast<const __half *>(slab + C::OFF_KN);
+            const __half * vn = reinterpret_cast<const __half *>(slab + C::OFF_VN);
+            // tokens with an infinite or NaN norm: their readers' sums are marked, and
+            // they take no part in the products
+            unsigned bad = 0u;
+            {
+                uint32_t x = 0u;
+                const uint32_t * kw = reinterpret_cast<const uint32_t *>(kn) + (lane & 15) * (NB / 2);
+                const uint32_t * vw = reinterpret_cast<const uint32_t *>(vn) + (lane & 15) * (NB / 2);
+                for (int i = 0; i < NB / 2; ++i) x |= ((kw[i] & 0x7C007C00u) + 0x04000400u) | ((vw[i] & 0x7C007C00u) + 0x04000400u);
+                bad = __ballot_sync(0xffffffffu, lane < 16 && (x & 0x80008000u) != 0u);
+                if (__builtin_expect(bad != 0u, 0)) {
+                    if ((bad >> lane) & 1u)
+                        for (int i = 0; i < NB / 2; ++i) {
+                            reinterpret_cast<uint32_t *>(slab + C::OFF_KN)[lane * (NB / 2) + i] = 0u;
+                            reinterpret_cast<uint32_t *>(slab + C::OFF_VN)[lane * (NB / 2) + i] = 0u;
+                        }
+                    __syncwarp();
+                }
+            }
+            float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};        // tokens g, g + 8 (k >> 1) of rows 2 t, 2 t + 1 (k & 1)
+            if (a.k_bits == 4) few_scores<D, 4>(x, slab, kn, qf, k_tab, g, t);
+            else if (a.k_bits == 3) few_scores<D, 3>(x, slab, kn, qf, k_tab, g, t);
+            else few_scores<D, 2>(x, slab, kn, qf, k_tab, g, t);
+            const int tok0 = t0 + 16 * s;
+            if (__builtin_expect(tok0 + 16 > ctx0 || bad != 0u, 0)) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int tok = tok0 + g + 8 * (k >> 1), nd = node[k & 1];
+                    bool ok = tok < p.rq.len;
+                    if (ok && tok >= ctx0) {
+                        const uint64_t * words = a.mask != nullptr ? a.mask + (int64_t)(p.rq.r0 + nd) * a.mask_words : nullptr;
+                        ok = (mask32(a, words, nd, tok - ctx0) & 1u) != 0u;
+                    }
+                    if (!ok) x[k] = -CUDART_INF_F;
+                    else if ((bad >> (g + 8 * (k >> 1))) & 1u) sum[k & 1] = CUDART_NAN_F;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] *= mul[k & 1];
+            // (a row with multiplier 0 is none: -inf times 0 stays in its own column)
+            const bool raise = fmaxf(x[0], x[2]) > ref[0] + fm::kLazy || fmaxf(x[1], x[3]) > ref[1] + fm::kLazy;
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float top = fmaxf(x[c], x[2 + c]);
+#pragma unroll
+                    for (int i = 4; i < 32; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+                    if (top > ref[c] + fm::kLazy) {
+                        const float f = ref[c] == -CUDART_INF_F ? 0.0f : fm::ex2(ref[c] - top);
+                        ref[c] = top;
+                        sum[c] *= f;
+#pragma unroll
+                        for (int i = 0; i < 2 * NB; ++i) {
+                            o[i][c] *= f;
+                            o[i][2 + c] *= f;
+                        }
+                    }
+                }
+            }
+            float w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float rf = ref[k & 1];
+                w[k] = fm::ex2(x[k] - (rf == -CUDART_INF_F ? 0.0f : rf) + fm::kShift<false>);
+                sum[k & 1] += w[k];
+            }
+            const uint32_t b0 = transpose_8x8(fm::pack2<false>(w[0], w[1])), b1 = transpose_8x8(fm::pack2<false>(w[2], w[3]));
+            const unsigned char * vc = slab + C::OFF_VC;
+            if (a.v_bits == 4) few_values<D, 4>(o, vc, vn, b0, b1, v_tab, g, t);
+            else if (a.v_bits == 3) few_values<D, 3>(o, vc, vn, b0, b1, v_tab, g, t);
+            else few_values<D, 2>(o, vc, vn, b0, b1, v_tab, g, t);
+            __syncwarp();                                 // the slab has been read
+            fetch(s + C::STAGES);
+            read_page(s + C::STAGES + 1);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
+        const bool own = p.tile0 == 0;
+        float * parts = own ? a.own : a.more;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float total = sum[c];
+#pragma unroll
+            for (int i = 4; i < 32; i <<= 1) total += __shfl_xor_sync(0xffffffffu, total, i);
+            const int r = 2 * t + c;
+            if (r >= p.rows) continue;
+            const int64_t at = own ? p.row_id + r : (int64_t)worker * a.more_rows + r;
+            if (g == 0) (own ? a.own_ml : a.more_ml)[at] = make_float2(ref[c], total);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                *reinterpret_cast<float4 *>(parts + part_at<D>(at, 32 * b + 4 * g)) =
+                    make_float4(o[2 * b][c], o[2 * b][2 + c], o[2 * b + 1][c], o[2 * b + 1][2 + c]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Merge and rotation back: R rows a CTA
 // ---------------------------------------------------------------------------
 
 constexpr int kTmThreads = 256;
 
-// First a lane has a row and a warp an eighth of the columns, so that the parts
-// are read as they were written (part_at); the sums meet in shared memory, and
-// every warp rotates four rows back.
-template <int D>
+// First the lanes of a warp have R rows and 32 / R groups of four columns, so
+// that the parts are read as they were written (part_at); the sums meet in shared
+// memory, and the warps rotate the rows back.  R = 8 where few rows share a key
+// tile: their parts are many (one per warp of the grid that shared the tiles), so
+// more CTAs read them, eight reads of a thread at a time (64 single tokens:
+// COMBINE32 us with R = 32, COMBINE8 with 8).
+template <int D, int R>
 __global__ void __launch_bounds__(kTmThreads) tree_combine_kernel(const __grid_constant__ TreeArgs a) {
-    constexpr int E = D / 32, NW = kTmThreads / 32, CH = D / 4 / NW, LD = D + 4, RW = 32 / NW;
-    __shared__ __align__(16) float y_s[32][LD];
-    __shared__ int64_t out_s[32];                        // where a row's output starts, -1: no row
+    constexpr int E = D / 32, NW = kTmThreads / 32, GP = 32 / R, LD = D + 4, RW = R / NW;
+    constexpr int CH = D / 4 >= NW * GP ? D / 4 / (NW * GP) : 1;
+    __shared__ __align__(16) float y_s[R][LD];
+    __shared__ int64_t out_s[R];                         // where a row's output starts, -1: no row
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t id = (int64_t)blockIdx.x * 32 + lane;
+    const int my_row = lane % R, my_col = 4 * (warp * GP + lane / R);      // and every 4 NW GP columns on
+    const bool active = my_col < D;
+    const int64_t id = (int64_t)blockIdx.x * R + my_row;
     wait_for_previous();
     // the row: its request, place in the request, and parts
     int64_t dst = -1, u0 = 0;
@@ -1048,7 +1394,7 @@ __global__ void __launch_bounds__(kTmThreads) tree_combine_kernel(const __grid_c
             }
         }
     }
-    if (warp == 0) out_s[lane] = dst;
+    if (warp == 0 && lane < R) out_s[lane] = dst;
     const int64_t units = a.unit0[a.batch], n = sharers(a, units);
     int c0 = 0, c1 = -1;                                 // the CTAs that share the row's tiles
     if (tiles > 0) {
@@ -1056,8 +1402,8 @@ __global__ void __launch_bounds__(kTmThreads) tree_combine_kernel(const __grid_c
         c1 = cta_of(u0 + tiles - 1, units, n);
     }
     // its parts, U at a time: their reads do not wait for one another
-    constexpr int U = D == 256 ? 2 : 4;
-    const int n_parts = (c1 - c0 + 1) * a.streams;
+    constexpr int U = R == 8 ? 8 : D == 256 ? 2 : 4;
+    const int n_parts = active ? (c1 - c0 + 1) * a.streams : 0;
     float ref = -CUDART_INF_F, sum = 0.0f;
     float4 acc[CH];
 #pragma unroll
@@ -1070,11 +1416,11 @@ __global__ void __launch_bounds__(kTmThreads) tree_combine_kernel(const __grid_c
             ml[u] = make_float2(-CUDART_INF_F, 0.0f);
             if (p0 + u < n_parts) {
                 const int at_c = a.streams == 2 ? (p0 + u) >> 1 : p0 + u, s = a.streams == 2 ? (p0 + u) & 1 : 0;
-                const int64_t at = at_c == 0 ? s * a.own_rows + id : (int64_t)(c0 + at_c) * (2 * kTile) + s * kTile + in_set;
+                const int64_t at = at_c == 0 ? s * a.own_rows + id : (int64_t)(c0 + at_c) * a.more_rows + s * kTile + in_set;
                 const float * parts = at_c == 0 ? a.own : a.more;
                 ml[u] = (at_c == 0 ? a.own_ml : a.more_ml)[at];
 #pragma unroll
-                for (int k = 0; k < CH; ++k) x[u][k] = *reinterpret_cast<const float4 *>(parts + part_at<D>(at, 4 * (k * NW + warp)));
+                for (int k = 0; k < CH; ++k) x[u][k] = *reinterpret_cast<const float4 *>(parts + part_at<D>(at, my_col + 4 * NW * GP * k));
             }
         }
 #pragma unroll
@@ -1100,7 +1446,7 @@ __global__ void __launch_bounds__(kTmThreads) tree_combine_kernel(const __grid_c
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
         if (isnan(sum)) acc[k] = make_float4(sum, sum, sum, sum);
-        *reinterpret_cast<float4 *>(&y_s[lane][4 * (k * NW + warp)]) = acc[k];
+        if (active) *reinterpret_cast<float4 *>(&y_s[my_row][my_col + 4 * NW * GP * k]) = acc[k];
     }
     __syncthreads();
     if (a.dense) {
@@ -1176,10 +1522,16 @@ int launch_tree(TreeArgs & a, cudaStream_t st) {
     tree_prep_kernel<D><<<vecs + 1, kTpThreads, 0, st>>>(a);
     if (int e = (int)cudaGetLastError()) return e;
     int e;
-    if constexpr (D == 256) e = launch_tree_main<D, WIDE>(a, st);
+    if (a.rows_per_set == kFewRows) {
+        using C = FewCfg<D>;
+        auto k = tree_few_kernel<D>;
+        if (int f = ensure_dynamic_smem(reinterpret_cast<const void *>(k), C::SMEM)) return f;
+        e = launch_dependent(k, (unsigned)(a.n_ctas / C::WARPS), 32 * C::WARPS, C::SMEM, st, a);
+    } else if constexpr (D == 256) e = launch_tree_main<D, WIDE>(a, st);
     else e = a.streams == 2 ? launch_tree_main<D, STREAM>(a, st) : launch_tree_main<D, PAIR>(a, st);
     if (e) return e;
-    return launch_dependent(tree_combine_kernel<D>, (unsigned)(a.own_rows / 32), kTmThreads, 0, st, a);
+    return a.rows_per_set == kFewRows ? launch_dependent(tree_combine_kernel<D, 8>, (unsigned)(a.own_rows / 8), kTmThreads, 0, st, a)
+                                      : launch_dependent(tree_combine_kernel<D, 32>, (unsigned)(a.own_rows / 32), kTmThreads, 0, st, a);
 }
 
 int64_t own_rows_of(int64_t vecs) { return (vecs + 31) / 32 * 32; }
@@ -1202,6 +1554,7 @@ TreeSpace tree_space(int64_t batch, int64_t n_rows, int64_t vecs, int d, int n_c
     s.q_mul = take((size_t)vecs * 4);
     s.own = take((size_t)own_rows_of(vecs) * 2 * d * 4);
     s.own_ml = take((size_t)own_rows_of(vecs) * 2 * 8);
+    // (16 warps with 8 rows each take half of what two row tiles do)
     s.more = take((size_t)n_ctas * 2 * kTile * d * 4);
     s.more_ml = take((size_t)n_ctas * 2 * kTile * 8);
     s.total = at;
@@ -1323,10 +1676,13 @@ extern "C" tq_status tq_tree_attention(const tq_rotation * rot, int32_t k_bits, 
     centroid_table(vcb, v_bits, a.v_table);
     a.group = n_q_heads / n_kv_heads;
     a.n_ctas = device_sm_count();
-    a.streams = head_dim < 256 && (int64_t)max_nodes * a.group <= kTile ? 2 : 1;
-    a.rows_per_set = head_dim < 256 && a.streams == 1 ? 2 * kTile : kTile;
+    const bool few = (int64_t)max_nodes * a.group <= kFewRows;
+    a.streams = !few && head_dim < 256 && (int64_t)max_nodes * a.group <= kTile ? 2 : 1;
+    a.rows_per_set = few ? kFewRows : head_dim < 256 && a.streams == 1 ? 2 * kTile : kTile;
+    a.more_rows = few ? kFewRows : 2 * kTile;
     unsigned char * ws = static_cast<unsigned char *>(workspace);
     const TreeSpace sp = tree_space(batch, n_rows, (int64_t)n_rows * n_q_heads, head_dim, a.n_ctas);
+    if (few) a.n_ctas *= head_dim == 256 ? FewCfg<256>::WARPS : FewCfg<128>::WARPS;
     a.unit0 = reinterpret_cast<int64_t *>(ws + sp.unit0);
     a.row_request = reinterpret_cast<int32_t *>(ws + sp.row_request);
     a.q_rows = reinterpret_cast<__half *>(ws + sp.q_rows);

@@ -429,6 +429,41 @@ def test_tree_many_requests(tq):
     _tree(tq, [1] * 150, lens, 2, 2, 64, 4, 4, 32, chain=True)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kb,vb", [(4, 3), (3, 4), (2, 2), (4, 4), (3, 3), (2, 4)])
+@pytest.mark.parametrize("dtype,kind", [("bf16", "wht"), ("f32", "haar")])
+def test_tree_few_rows(tq, d, kb, vb, dtype, kind):
+    """At most 8 rows share a key tile: a kernel of its own."""
+    _tree(tq, [1, 2, 0, 1, 2], [300, 17, 5, 1, 1999], 8, 2, d, kb, vb, 16, dtype=dtype, kind=kind)
+    _tree(tq, [1] * 6, [128, 16, 15, 129, 3000, 7], 7, 1, d, kb, vb, 64, chain=True, dtype=dtype, pad=2)
+
+
+def test_tree_few_rows_masks_and_bad_norms(tq):
+    masks = [[0b00001, 0, 0b00100, 0b11111, 0b00011], [0b01, 0b10]]
+    g, ref = _tree(tq, [5, 2], [5, 60], 1, 1, 128, 4, 3, 16, masks=masks)
+    assert np.all(g[1] == 0)
+
+    def edit(pages, table):
+        page = pages["v_norms"].shape[2]
+        for name, t, what in (("k_norms", 61, "nan"), ("v_norms", 30, "inf")):
+            pages[name][table[0, t // page], 0, t % page, 2] = np.float16(what)
+            pages[name][table[0, 63 // page], 1, 64 % page:] = np.float16("nan")
+    g, ref = _tree(tq, [4], [64], 2, 2, 128, 4, 3, 32, masks=[[0b0001, 0b0011, 0b0101, 0b1011]], edit=edit)
+    assert np.isnan(g).all()          # token 30 of head 0 and the second page of head 1 are every node's
+
+    def drafted(pages, table):
+        page = pages["v_norms"].shape[2]
+        pages["v_norms"][table[0, 61 // page], :, 61 % page, 0] = np.float16("inf")
+    g, ref = _tree(tq, [4], [64], 2, 2, 64, 3, 2, 16, masks=[[0b0001, 0b0011, 0b0101, 0b1011]], edit=drafted)
+    assert np.isfinite(g[[0, 2]]).all() and not np.isfinite(g[[1, 3]]).any()
+
+
+def test_tree_few_rows_long_and_many(tq):
+    rng = np.random.default_rng(8)
+    lens = [int(x) for x in rng.integers(0, 700, 300)] + [20000]
+    _tree(tq, [min(1, x) for x in lens], lens, 4, 1, 64, 4, 3, 64, chain=True)
+
+
 def test_tree_more_requests_than_a_search_step(tq):
     rng = np.random.default_rng(5)
     nodes = rng.integers(0, 3, 1100).tolist()
@@ -576,7 +611,7 @@ def test_tree_captured_twice_and_replayed(tq):
 @pytest.mark.parametrize("d,hq", [(128, 8), (128, 4), (256, 8), (64, 8)])
 def test_tree_runs_agree_bit_for_bit(tq, d, hq):
     rng = np.random.default_rng(d + hq)
-    page, nodes, lens = 64, [30, 1, 64], [3000, 129, 900]
+    page, lens = 64, [3000, 129, 900]
     table, n_pages = S.page_tables_for(rng, lens, page)
     pages = S.cache_to(S.random_cache(rng, n_pages, 2, page, d, 4, 3), "cuda")
     kc, vc = tq.build_codebook(4)[0], tq.build_codebook(3)[0]
