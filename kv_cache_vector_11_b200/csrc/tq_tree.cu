@@ -1058,20 +1058,27 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t table_at(uint32_t addr) {
-    uint32_t v;
-    asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));      // (written before the first unit only)
-    return v;
+// The pair tables: entry e (two codes, the first in its low bits) at byte 256 e,
+// keys in the lower half, values in the upper, one word a lane.  Offset of the
+// pair at bit `sh` of x: the pair's bits at bit 8 on, the lane's word below; for
+// 4-bit codes, whose pairs are bytes, one byte permute.
+template <int BITS>
+__device__ __forceinline__ uint32_t pair_at(uint32_t x, int sh, uint32_t lane4) {
+    if constexpr (BITS == 4) {
+        return __byte_perm(x, lane4, 0x7704u | ((uint32_t)(sh >> 3) << 4));
+    } else {
+        constexpr uint32_t MASK = ((1u << (2 * BITS)) - 1u) << 8;
+        return ((sh >= 8 ? x >> (sh - 8) : x << (8 - sh)) & MASK) | lane4;
+    }
 }
 
 // Scores of 16 tokens: acc += keys x queries.  `codes`: the slab's packed keys,
-// qf: the lane's query words (B fragments in order), tab: the lane's copy.
+// qf: the lane's query words (B fragments in order).
 template <int D, int BITS>
 __device__ __forceinline__ void few_scores(float * acc, const unsigned char * codes, const __half * norms, const uint32_t * qf,
-                                           uint32_t tab, int g, int t) {
+                                           const unsigned char * tables, uint32_t lane4, int g, int t) {
     constexpr int NB = D / 32, SEG = D / 4, ROW = D / 8 * BITS;
     constexpr int PIECE = SEG < 32 ? SEG : 32;           // codes taken at a time: a block, or half of one
-    constexpr uint32_t MASK = (1u << (2 * BITS)) - 1u;
 #pragma unroll
     for (int b = 0; b < SEG / PIECE; ++b) {
         const int blk = D == 64 ? t >> 1 : t * (SEG / 32) + b;
@@ -1100,8 +1107,9 @@ __device__ __forceinline__ void few_scores(float * acc, const unsigned char * co
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int bit = 2 * BITS * (2 * k + h), wi = bit >> 5, sh = bit & 31;
-                    const uint32_t x = sh + 2 * BITS <= 32 ? w[r][wi] >> sh : __funnelshift_r(w[r][wi], w[r][wi + 1], sh);
-                    a[2 * h + r] = hmul2_u(table_at(tab + (x & MASK) * 128u), norm[r]);
+                    const uint32_t at = sh + 2 * BITS <= 32 ? pair_at<BITS>(w[r][wi], sh, lane4)
+                                                            : pair_at<BITS>(__funnelshift_r(w[r][wi], w[r][wi + 1], sh - 8), 8, lane4);
+                    a[2 * h + r] = hmul2_u(*reinterpret_cast<const uint32_t *>(tables + at), norm[r]);
                 }
             mma_16816(acc, a, qf[2 * (b * (PIECE / 4) + k)], qf[2 * (b * (PIECE / 4) + k) + 1]);
         }
@@ -1111,10 +1119,16 @@ __device__ __forceinline__ void few_scores(float * acc, const unsigned char * co
 // Output of 16 tokens: o += values x weights (b0, b1: the lane's weights).
 template <int D, int BITS>
 __device__ __forceinline__ void few_values(float (*o)[4], const unsigned char * codes, const __half * norms, uint32_t b0, uint32_t b1,
-                                           uint32_t tab, int g, int t) {
+                                           const unsigned char * tables, uint32_t lane4, int g, int t) {
     constexpr int NB = D / 32, ROW = D / 8 * BITS;
-    constexpr uint32_t MASK = (1u << (2 * BITS)) - 1u;
     const int bit = 4 * BITS * g, wi = bit >> 5, sh = bit & 31;       // the lane's 4 codes of a block
+    // norms of the four tokens, all blocks, two to a word
+    uint32_t nw[4][NB / 2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i)
+            nw[k][i] = reinterpret_cast<const uint32_t *>(norms + (2 * t + (k & 1) + 8 * (k >> 1)) * NB)[i];
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk) {
         uint32_t lo[4], hi[4];                            // (coordinate 0, 1) and (2, 3) of the four tokens
@@ -1125,14 +1139,14 @@ __device__ __forceinline__ void few_values(float (*o)[4], const unsigned char * 
             uint32_t x = row[wi];
             if (BITS == 3) x = __funnelshift_r(x, row[min(wi + 1, 2)], sh);
             else x >>= sh;
-            lo[k] = table_at(tab + (x & MASK) * 128u);
-            hi[k] = table_at(tab + ((x >> (2 * BITS)) & MASK) * 128u);
+            lo[k] = *reinterpret_cast<const uint32_t *>(tables + 128 + pair_at<BITS>(x, 0, lane4));
+            hi[k] = *reinterpret_cast<const uint32_t *>(tables + 128 + pair_at<BITS>(x, 2 * BITS, lane4));
         }
         uint32_t a0[4], a1[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {                     // tokens 2 t, 2 t + 1; then those 8 on
-            const int tok = 2 * t + 8 * h;
-            const __half2 norm = __halves2half2(norms[tok * NB + blk], norms[(tok + 1) * NB + blk]);
+            const uint32_t nn = __byte_perm(nw[2 * h][blk >> 1], nw[2 * h + 1][blk >> 1], blk & 1 ? 0x7632 : 0x5410);
+            const __half2 norm = *reinterpret_cast<const __half2 *>(&nn);
             a0[2 * h] = hmul2_u(__byte_perm(lo[2 * h], lo[2 * h + 1], 0x5410), norm);
             a0[2 * h + 1] = hmul2_u(__byte_perm(lo[2 * h], lo[2 * h + 1], 0x7632), norm);
             a1[2 * h] = hmul2_u(__byte_perm(hi[2 * h], hi[2 * h + 1], 0x5410), norm);
@@ -1153,8 +1167,8 @@ __global__ void __launch_bounds__(32 * FewCfg<D>::WARPS, 1) tree_few_kernel(cons
     let_next_start();
     // the pair tables
     for (int i = threadIdx.x; i < 2 * 256 * 32; i += 32 * C::WARPS) {
-        const bool v = i >= 256 * 32;
-        const int e = (i >> 5) & 255, bits = v ? a.v_bits : a.k_bits;
+        const bool v = (i & 32) != 0;
+        const int e = i >> 6, bits = v ? a.v_bits : a.k_bits;
         const uint32_t * tab = v ? a.v_table : a.k_table;
         auto entry = [&](int c) {
             return ((tab[c >> 2] >> (8 * (c & 3))) & 0xFFu) | ((tab[4 + (c >> 2)] >> (8 * (c & 3))) & 0xFFu) << 8;
@@ -1164,7 +1178,7 @@ __global__ void __launch_bounds__(32 * FewCfg<D>::WARPS, 1) tree_few_kernel(cons
     wait_for_previous();
     __syncthreads();
     const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(smem);
-    const uint32_t k_tab = sbase + 4u * (uint32_t)lane, v_tab = k_tab + 256u * 128u;
+    const uint32_t lane4 = 4u * (uint32_t)lane;
     const uint32_t ring = (uint32_t)(C::OFF_RING + warp * C::STAGES * C::SLAB);
 
     // this warp's units
@@ -1277,9 +1291,9 @@ __global__ void __launch_bounds__(32 * FewCfg<D>::WARPS, 1) tree_few_kernel(cons
                 }
             }
             float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};        // tokens g, g + 8 (k >> 1) of rows 2 t, 2 t + 1 (k & 1)
-            if (a.k_bits == 4) few_scores<D, 4>(x, slab, kn, qf, k_tab, g, t);
-            else if (a.k_bits == 3) few_scores<D, 3>(x, slab, kn, qf, k_tab, g, t);
-            else few_scores<D, 2>(x, slab, kn, qf, k_tab, g, t);
+            if (a.k_bits == 4) few_scores<D, 4>(x, slab, kn, qf, smem, lane4, g, t);
+            else if (a.k_bits == 3) few_scores<D, 3>(x, slab, kn, qf, smem, lane4, g, t);
+            else few_scores<D, 2>(x, slab, kn, qf, smem, lane4, g, t);
             const int tok0 = t0 + 16 * s;
             if (__builtin_expect(tok0 + 16 > ctx0 || bad != 0u, 0)) {
 #pragma unroll
@@ -1325,9 +1339,9 @@ __global__ void __launch_bounds__(32 * FewCfg<D>::WARPS, 1) tree_few_kernel(cons
             }
             const uint32_t b0 = transpose_8x8(fm::pack2<false>(w[0], w[1])), b1 = transpose_8x8(fm::pack2<false>(w[2], w[3]));
             const unsigned char * vc = slab + C::OFF_VC;
-            if (a.v_bits == 4) few_values<D, 4>(o, vc, vn, b0, b1, v_tab, g, t);
-            else if (a.v_bits == 3) few_values<D, 3>(o, vc, vn, b0, b1, v_tab, g, t);
-            else few_values<D, 2>(o, vc, vn, b0, b1, v_tab, g, t);
+            if (a.v_bits == 4) few_values<D, 4>(o, vc, vn, b0, b1, smem, lane4, g, t);
+            else if (a.v_bits == 3) few_values<D, 3>(o, vc, vn, b0, b1, smem, lane4, g, t);
+            else few_values<D, 2>(o, vc, vn, b0, b1, smem, lane4, g, t);
             __syncwarp();                                 // the slab has been read
             fetch(s + C::STAGES);
             read_page(s + C::STAGES + 1);
