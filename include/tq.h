@@ -555,9 +555,10 @@ tq_status tq_quantize_kv_paged(const tq_rotation * rot, int32_t bits, int32_t bl
  *   out:        device [total_q][n_q_heads][head_dim] of dtype, contiguous, 16-byte
  *               aligned; rows from cu_q[batch] on are left as they are.
  *   status_dev: device uint32 or NULL (TQ_STATUS_TIMEOUT).
- * head_dim 64 / 128 / 256; n_q_heads a multiple of n_kv_heads; any group size.
- * Scores and sums are fp32; the probabilities enter the second product rounded
- * to dtype, the sum that divides them does not.
+ * head_dim 64 / 128 / 256; n_q_heads a multiple of n_kv_heads; any group size;
+ * total_q and total_k below 2^31 - 255.  Scores and sums are fp32; the
+ * probabilities enter the second product rounded to dtype, the sum that divides
+ * them does not.
  */
 tq_status tq_prompt_attention(const void * q, const void * k, const void * v, tq_dtype dtype,
                               const int32_t * cu_q, const int32_t * cu_k, int32_t batch,
@@ -595,11 +596,12 @@ size_t tq_tree_workspace_size(int32_t batch, int32_t n_rows, int32_t max_nodes,
  *               at most max_nodes apart (1 <= max_nodes <= 256; nodes from
  *               max_nodes on are left out; offsets are clamped to [0, n_rows]).
  *   lens:       device int32 [batch], 0 .. max_len (clamped); max_len <=
- *               max_pages * page_size.
+ *               max_pages * page_size, and below 2^31 - 255.
  *   tree_mask:  device uint64 [n_rows][mask_words] or NULL; mask_words >=
  *               ceil(max_nodes / 64).
  *   block_table, page_size, n_pages, k_*, v_*: as in tq_decode_append_paged
- *               (entries outside [0, n_pages) are clamped).
+ *               (entries outside [0, n_pages) are clamped), fewer than 2^32 rows
+ *               (n_pages * n_kv_heads * page_size).
  *   out:        device [n_rows][n_q_heads][head_dim] of q_dtype, 16-byte aligned.
  *   workspace:  >= tq_tree_workspace_size(...) bytes for these sizes, 256-byte
  *               aligned, needs no initialisation; calls that may overlap need one

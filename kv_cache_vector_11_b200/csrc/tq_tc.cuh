@@ -139,17 +139,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t saddr, uint32_t parity, uint6
     return false;
 }
 
-// Whether the phase with the given parity is complete; does not wait.
-__device__ __forceinline__ bool mbar_test(uint32_t saddr, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(done) : "r"(saddr), "r"(parity) : "memory");
-    return done != 0u;
-}
-
 // Plain mbarrier arrive (count 1).
 __device__ __forceinline__ void mbar_arrive(uint32_t saddr) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(saddr) : "memory");

@@ -17,22 +17,27 @@
 // it writes its part of the sum into a slot of its own, all other parts go to
 // the rows' own slots, so a row has one own slot and one more per further CTA.
 //
-// In the CTA four warps unpack codes into the swizzled operand tiles (shared
-// memory, a ring of buffers), two threads issue the MMAs, one softmax thread
-// per row turns scores into weights (tq_fmha.cuh).  Which rows share a CTA:
+// In the CTA one warpgroup unpacks keys and one values into swizzled operand tiles
+// (shared memory, a ring of buffers each), two warps issue the MMAs, one softmax
+// thread per row turns scores into weights (tq_fmha.cuh).  Which rows share a CTA:
 //   PAIR:   two row tiles (256 rows) against the same key tile: unpacking is
 //           paid once for both, the tensor core works on one while the softmax
 //           warps of the other run;
 //   STREAM: one row tile (at most 128 rows), the even key tiles and the odd
-//           ones with a softmax and an accumulator each: half the unpacking is
-//           hidden behind twice the softmax throughput.  Taken when no request
+//           ones with a softmax and an accumulator each.  Taken when no request
 //           can have more than 128 rows;
 //   WIDE:   d = 256, one row tile whose accumulator fills half of TMEM, the
 //           scores of the next key tile under way during a softmax.
+// At most 8 rows take a kernel of their own (tree_few_kernel).
 //
 // Unpacking: centroids are 16-bit table entries, looked up four at a time with
 // byte permutes (a table of 8 bytes in two registers; the low and the high
 // bytes of four entries, interleaved), times the block's norm in fp16.
+//
+// What bounds it: the integer pipe, which byte permutes, masks and the maxima of
+// the softmax share.  A key tile of 128 tokens takes the two unpacking warpgroups
+// about 3000 cycles (d = 128, 4-bit keys and 3-bit values), its products 1280 a
+// row tile; 8 x 128K trees of 64 nodes, 4 heads a group: 1.21 ms, 0.91 PFLOP/s.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -125,8 +130,8 @@ __device__ __forceinline__ int cta_of(int64_t u, int64_t units, int64_t n) {
 
 // Where column `col` (a multiple of 4) of row `row` of the partial sums lies:
 // 32 rows take turns, four columns each, since a thread has a row and a warp
-// then writes 512 bytes in a piece (row by row, 16 bytes of 32 rows at a time,
-// the accumulators take ROWWISE cycles to write, this way COLWISE).
+// then writes 512 bytes in a piece (stored row by row, 16 bytes of 32 rows at a
+// time, tree_kernel took 130 us for 16 trees over up to 32K tokens, this way 114).
 template <int D>
 __device__ __forceinline__ int64_t part_at(int64_t row, int col) {
     return ((row >> 5) * (D / 4) + (col >> 2)) * 128 + (row & 31) * 4;
@@ -1033,7 +1038,12 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
 // Pairs of codes become pairs of fp16 centroids by one shared-memory lookup (a
 // copy of the table per lane, so no two lanes meet in a bank), times the norm.
 // The units are shared among the warps of the grid as they are among its CTAs
-// elsewhere.  FEWTIME
+// elsewhere.
+//
+// 64 single tokens over 1 .. 32K tokens (133 MB of packed rows, 20 us of HBM time):
+// 66 us, 214 us with tree_kernel.  Bound by the issue slots (77 % busy: some 600
+// instructions per 16 tokens, a third of them lookups); the ring keeps three
+// slabs a warp on their way.
 template <int D>
 struct FewCfg {
     static constexpr int NB = D / 32, SEG = D / 4;       // blocks; coordinates of a lane's run of keys
@@ -1377,8 +1387,8 @@ constexpr int kTmThreads = 256;
 // that the parts are read as they were written (part_at); the sums meet in shared
 // memory, and the warps rotate the rows back.  R = 8 where few rows share a key
 // tile: their parts are many (one per warp of the grid that shared the tiles), so
-// more CTAs read them, eight reads of a thread at a time (64 single tokens:
-// COMBINE32 us with R = 32, COMBINE8 with 8).
+// more CTAs read them, eight reads of a thread at a time (rotation and
+// merge of 64 single tokens: 36 us with R = 32, 20 us with 8).
 template <int D, int R>
 __global__ void __launch_bounds__(kTmThreads) tree_combine_kernel(const __grid_constant__ TreeArgs a) {
     constexpr int E = D / 32, NW = kTmThreads / 32, GP = 32 / R, LD = D + 4, RW = R / NW;
