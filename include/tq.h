@@ -553,7 +553,8 @@ tq_status tq_quantize_kv_paged(const tq_rotation * rot, int32_t bits, int32_t bl
  *               cu_k NULL = cu_q.
  *   scale:      <= 0 selects 1/sqrt(head_dim).
  *   out:        device [total_q][n_q_heads][head_dim] of dtype, contiguous, 16-byte
- *               aligned; rows from cu_q[batch] on are left as they are.
+ *               aligned; rows from cu_q[batch] on are left as they are.  Must not
+ *               overlap q, k or v.
  *   status_dev: device uint32 or NULL (TQ_STATUS_TIMEOUT).
  * head_dim 64 / 128 / 256; n_q_heads a multiple of n_kv_heads; any group size;
  * total_q and total_k below 2^31 - 255.  Scores and sums are fp32; the

@@ -213,7 +213,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             if (hit != 0u) {
                 const int at = __ffs((int)hit) - 1;
                 seq = b0 + at;
-                tile = __shfl_sync(0xffffffffu, end, at) - 1 - tau;
+                // (inside the sequence whatever the offsets are)
+                tile = max(min(__shfl_sync(0xffffffffu, end, at) - 1 - tau, __shfl_sync(0xffffffffu, nt, at) - 1), 0);
                 q0 = __shfl_sync(0xffffffffu, r0, at);
                 q1 = __shfl_sync(0xffffffffu, r1, at);
                 k0 = __shfl_sync(0xffffffffu, c0, at);
@@ -657,6 +658,7 @@ extern "C" tq_status tq_prompt_attention(const void * q, const void * k, const v
     if (total_q == 0) return TQ_OK;
     if (!q || !out || !cu_q || (total_k > 0 && (!k || !v)))
         return fail(TQ_ERR_INVALID_ARG, "null q / k / v / out / cu_q");
+    if (out == q || out == k || out == v) return fail(TQ_ERR_INVALID_ARG, "out must not be q, k or v");
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_q, 4) ||
         !aligned(cu_k, 4) || !aligned(status_dev, 4))
         return fail(TQ_ERR_INVALID_ARG, "q, k, v and out must be 16-byte aligned, offsets 4-byte");

@@ -59,7 +59,7 @@ def test_quantize_paged_refusals(rot, kw, code):
 
 
 def prompt(q=FAKE, k=FAKE, v=FAKE, dtype=1, cu_q=FAKE, cu_k=None, batch=2, tq_=8, tk=8, hq=4, hk=2, d=128, qs=512,
-           ks=256, vs=256, scale=0.0, out=FAKE):
+           ks=256, vs=256, scale=0.0, out=FAKE + 4096):
     return L.tq_prompt_attention(q, k, v, dtype, cu_q, cu_k, batch, tq_, tk, hq, hk, d, qs, ks, vs, scale, out, None,
                                  None)
 
@@ -71,7 +71,7 @@ def prompt(q=FAKE, k=FAKE, v=FAKE, dtype=1, cu_q=FAKE, cu_k=None, batch=2, tq_=8
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(out=None), INVALID), (dict(cu_q=None), INVALID),
     (dict(q=FAKE + 8), INVALID), (dict(out=FAKE + 8), INVALID), (dict(cu_k=FAKE + 2), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(tq_=0, q=None), OK),
-    (dict(tq_=2**31 - 200), UNSUPPORTED), (dict(tk=2**31 - 200, cu_k=FAKE), UNSUPPORTED),
+    (dict(out=FAKE), INVALID), (dict(tq_=2**31 - 200), UNSUPPORTED), (dict(tk=2**31 - 200, cu_k=FAKE), UNSUPPORTED),
     (dict(batch=2**31 - 1, hq=4, hk=4, ks=512, vs=512), UNSUPPORTED),
 ])
 def test_prompt_refusals(kw, code):
