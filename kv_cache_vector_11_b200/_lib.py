@@ -404,19 +404,26 @@ def _host_floats(x):
     return a, a.__array_interface__["data"][0]
 
 
+def _stream_of(device):
+    """Handle of the current stream of a CUDA device.  Read without building a
+    Stream object (2 us of a call that takes 12) where torch offers that."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+
+
 def _launch(fn, where, device, stream, *args):
     """fn(*args, stream) with ``device`` current (as _on; a serving step makes
     many short calls, so nothing is switched that is current already)."""
     import torch
     if device.type != "cuda":
         raise ValueError(f"{where}: tensors on {device}, not on a CUDA device")
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
+    handle = _stream_of(device) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == device.index:
-        status = fn(*args, stream.cuda_stream)
+        status = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            status = fn(*args, stream.cuda_stream)
+            status = fn(*args, handle)
     if status != 0:
         raise TQError(status, where)
 
