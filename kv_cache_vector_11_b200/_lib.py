@@ -412,6 +412,16 @@ def _stream_of(device):
     return raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
+def _made_for(stream, *tensors):
+    """Tensors that a call allocated (on the current stream) and hands to a
+    launch on ``stream``: their memory is not given out again before that
+    stream is done with them."""
+    if stream is not None:
+        for t in tensors:
+            if t.is_cuda:
+                t.record_stream(stream)
+
+
 def _launch(fn, where, device, stream, *args):
     """fn(*args, stream) with ``device`` current (as _on; a serving step makes
     many short calls, so nothing is switched that is current already)."""
@@ -448,6 +458,7 @@ def page_tables(ctx_lens, new_lens, page_size, n_pages, free_pages, block_table,
                "slots": torch.empty((n_slots,), dtype=torch.int64, device=dev),
                "positions": torch.empty((n_slots,), dtype=torch.int32, device=dev),
                "n_taken": torch.empty((1,), dtype=torch.int32, device=dev)}
+        _made_for(stream, *out.values())
     i32 = torch.int32
     _require(block_table.dim() == 2 and block_table.shape[0] == batch, "block_table: [batch, max_pages]")
     n_free, max_pages = free_pages.numel(), block_table.shape[1]
@@ -503,6 +514,7 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, scale=0.0, out=None, status=None,
     dev = q.device
     if out is None:
         out = torch.empty((total_q, n_q, d), dtype=q.dtype, device=dev)
+        _made_for(stream, out)
     for name, t, n, h in (("q", q, total_q, n_q), ("k", k, total_k, n_kv), ("v", v, total_k, n_kv)):
         _require(tuple(t.shape) == (n, h, d) and t.dtype == q.dtype and t.device == dev and
                  t.stride(2) == 1 and (h == 1 or t.stride(1) == d),
@@ -544,6 +556,7 @@ def tree_attention(rot, k_bits, v_bits, k_centroids, v_centroids, q, cu_nodes, l
     batch = lens.shape[0]
     if out is None:
         out = torch.empty((n_rows, n_q, d), dtype=q.dtype, device=dev)
+        _made_for(stream, out)
     _require(q.is_contiguous() and out.shape == q.shape and out.dtype == q.dtype and
              out.is_contiguous() and out.device == dev, "q and out: contiguous, same shape and type")
     cu_p = _ints(cu_nodes, batch + 1, "cu_nodes", dev, torch.int32)
@@ -571,6 +584,7 @@ def tree_attention(rot, k_bits, v_bits, k_centroids, v_centroids, q, cu_nodes, l
         with _on(dev):
             need = tree_workspace_size(batch, n_rows, max_nodes, n_q, n_kv, max_len, d)
             workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
+        _made_for(stream, workspace)
     _launch(_lib.tq_tree_attention, "tq_tree_attention", dev, stream, rot.handle, k_bits, v_bits, block, kc_p,
             vc_p, _ptr(q), _dtype_code16(q), cu_p, batch, n_rows, max_nodes, lens_p, max_len, mask_p, words,
             n_q, n_kv, d, page_size, n_pages, table_p, block_table.shape[1], _ptr(pages["k_codes"]),

@@ -333,6 +333,33 @@ def test_prompt_and_tree_on_two_streams_at_once(tq):
     assert all(torch.equal(a, b) for a, b in got)
 
 
+def test_memory_of_a_call_is_kept_for_the_stream_it_runs_on(tq):
+    """stream= another than the current one, workspace and outputs left to the call: what is allocated
+    after the call, while that stream is still busy, does not get its memory."""
+    rng = np.random.default_rng(12)
+    d, page = 128, 32
+    table, n_pages = S.page_tables_for(rng, [2000, 700], page)
+    pages = S.cache_to(S.random_cache(rng, n_pages, 2, page, d, 4, 3), "cuda")
+    rot = tq.Rotation("wht", d, d, W.SEED_ROT)
+    kc, vc = tq.build_codebook(4)[0], tq.build_codebook(3)[0]
+    q = torch.randn((60, 8, d), device="cuda").bfloat16()
+    cu, lens, tab = i32([0, 40, 60]), i32([2000, 700]), i32(table)
+    need = tq.tree_workspace_size(2, 60, 40, 8, 2, 2000, d)
+
+    def tree(**kw):
+        return tq.tree_attention(rot, 4, 3, kc, vc, q, cu, lens, pages, tab, page, 40, 2000, **kw)
+    want = tree()
+    side, x = torch.cuda.Stream(), torch.randn((4096, 4096), device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            x = x @ x * 1e-2
+    got = tree(stream=side)
+    later = [torch.full((need,), 0x3C, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and all(bool((t == 0x3C).all()) for t in later)
+
+
 # -- drafted tokens over the cache ------------------------------------------------------------
 
 def _tree(tq, nodes, lens, hq, hk, d, kb, vb, page, dtype="bf16", kind="wht", chain=False, seed=0, masks=None, scale=0.0,
