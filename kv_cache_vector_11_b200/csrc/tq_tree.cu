@@ -125,7 +125,7 @@ __device__ __forceinline__ int64_t first_unit(int64_t c, int64_t units, int64_t 
 __device__ __forceinline__ int cta_of(int64_t u, int64_t units, int64_t n) {
     const int64_t x = (u + 1) * n - 1;
     // (a 32-bit division where it does: the 64-bit one takes some 500 cycles)
-    return x <= 0xFFFFFFFFll ? (int)((uint32_t)x / (uint32_t)units) : (int)(x / units);
+    return (x | units) <= 0xFFFFFFFFll ? (int)((uint32_t)x / (uint32_t)units) : (int)(x / units);
 }
 
 // Where column `col` (a multiple of 4) of row `row` of the partial sums lies:
