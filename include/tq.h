@@ -498,6 +498,7 @@ tq_status tq_search_topk(const tq_rotation * rot, int32_t bits, int32_t block,
  *   n_taken:    device int32 [1], out: pages taken; free_pages[0 .. n_taken) now
  *               belong to the requests.
  *   status_dev: device uint32 or NULL.
+ * No output may overlap an input (every block reads the lengths) or another output.
  * A request is placed if its pages fit its table row (want <= max_pages), its
  * tokens fit the slot map (cu_new[b + 1] <= n_slots), ctx + new < 2^31, and the
  * pages needed up to and including it fit the free list; otherwise none of its

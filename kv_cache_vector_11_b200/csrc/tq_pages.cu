@@ -182,8 +182,8 @@ extern "C" tq_status tq_page_tables(const int32_t * ctx_lens, const int32_t * ne
     if (n_free < 0 || n_slots < 0) return fail(TQ_ERR_INVALID_ARG, "n_free and n_slots must be >= 0");
     if (!ctx_lens || !new_lens || !block_table || !cu_new || !total_lens || !n_taken)
         return fail(TQ_ERR_INVALID_ARG, "null lengths / block_table / cu_new / total_lens / n_taken");
-    if (total_lens == ctx_lens || total_lens == new_lens)
-        return fail(TQ_ERR_INVALID_ARG, "total_lens must not be an input array");
+    if (total_lens == ctx_lens || total_lens == new_lens || cu_new == ctx_lens || cu_new == new_lens)
+        return fail(TQ_ERR_INVALID_ARG, "total_lens and cu_new must not be input arrays");
     if ((n_free > 0 && !free_pages) || (n_slots > 0 && !slots))
         return fail(TQ_ERR_INVALID_ARG, "null free_pages / slots");
     if (!aligned(ctx_lens, 4) || !aligned(new_lens, 4) || !aligned(free_pages, 4) || !aligned(block_table, 4) ||

@@ -40,6 +40,15 @@ def test_page_tables_refusals(kw, code):
     assert tables(**kw) == code and tq.TQError(code, "x").args
 
 
+@pytest.mark.parametrize("alias", ["ctx", "new"])
+def test_page_tables_refuses_outputs_over_the_lengths(alias):
+    apart = dict(ctx=FAKE, new=FAKE + 1024, cu=FAKE + 2048, total=FAKE + 4096)
+    assert tables(**dict(apart, free=None)) == INVALID and "free_pages" in L.tq_last_error().decode()
+    for out in ("cu", "total"):
+        assert tables(**dict(apart, **{out: apart[alias]}, free=None)) == INVALID
+        assert "input" in L.tq_last_error().decode()
+
+
 def paged(rot, bits=4, block=32, x=FAKE, dtype=1, n=4, heads=2, d=128, slots=FAKE, page=16, n_pages=8, codes=FAKE,
           norms=FAKE, c=None, t=None):
     kc, kt = tq.build_codebook(max(bits, 1), 32)
