@@ -391,17 +391,25 @@ def _dtype_code16(t):
 
 def _ints(t, n, name, device, kind):
     """Pointer of a contiguous integer array of n entries on ``device`` (the
-    kernels read it without further checks)."""
+    kernels read it without further checks).  Here and below a message is put
+    together only where it is raised (the strings of calls that pass were 4 of
+    the 10 us that prompt_attention's checks took)."""
     if not (t.dtype is kind and t.numel() == n and t.is_contiguous() and t.device == device):
         raise ValueError(f"{name}: contiguous {kind} of {n} entries on {device}")
     return t.data_ptr()
 
 
+def _page_part(t, name, kind, shape, device):
+    """Pointer of one array of the page storage, [page][kv head][token][..]."""
+    if not (t.shape == shape and t.dtype is kind and t.is_contiguous() and t.device == device):
+        raise ValueError(f"{name}: contiguous {kind} {list(shape)} on {device}")
+    return t.data_ptr()
+
+
 def _host_floats(x):
-    """(array that keeps it alive, pointer) of a contiguous fp32 copy or view of
-    x (``ndarray.ctypes`` builds an object a call, several times slower)."""
-    a = np.ascontiguousarray(x, dtype=np.float32)
-    return a, a.__array_interface__["data"][0]
+    """x as fp32 in a bytes object, which ctypes passes as a pointer (0.3 us; an
+    array's address by ``ndarray.ctypes`` takes several times that)."""
+    return np.ascontiguousarray(x, dtype=np.float32).tobytes()
 
 
 def _stream_of(device):
@@ -489,16 +497,11 @@ def quantize_kv_paged(rot, bits, centroids, boundaries, x, slots, codes, norms, 
     w = d * bits // 32                                  # (the library refuses other blocks and widths)
     _require(x.is_contiguous(), "x: contiguous [n_tokens, n_kv_heads, head_dim]")
     slots_p = _ints(slots, n, "slots", dev, torch.int64)
-    _require(tuple(codes.shape) == (n_pages, heads, page_size, w) and codes.dtype == torch.int32 and
-             codes.is_contiguous() and codes.device == dev, f"codes: int32 [n_pages, {heads}, {page_size}, {w}]")
-    _require(tuple(norms.shape) == (n_pages, heads, page_size, d // 32) and norms.dtype == torch.int16 and
-             norms.is_contiguous() and norms.device == dev,
-             f"norms: int16 [{n_pages}, {heads}, {page_size}, {d // 32}]")
-    c, c_p = _host_floats(centroids)
-    t, t_p = _host_floats(boundaries)
-    _launch(_lib.tq_quantize_kv_paged, "tq_quantize_kv_paged", dev, stream, rot.handle, bits, block, c_p,
-            t_p, _ptr(x), _dtype_code(x), n, heads, d, slots_p, page_size, n_pages, _ptr(codes), _ptr(norms),
-            _ptr(status))
+    codes_p = _page_part(codes, "codes", torch.int32, (n_pages, heads, page_size, w), dev)
+    norms_p = _page_part(norms, "norms", torch.int16, (n_pages, heads, page_size, d // 32), dev)
+    _launch(_lib.tq_quantize_kv_paged, "tq_quantize_kv_paged", dev, stream, rot.handle, bits, block,
+            _host_floats(centroids), _host_floats(boundaries), x.data_ptr(), _dtype_code(x), n, heads, d,
+            slots_p, page_size, n_pages, codes_p, norms_p, _ptr(status))
 
 
 def prompt_attention(q, k, v, cu_q, cu_k=None, scale=0.0, out=None, status=None, stream=None):
@@ -515,11 +518,15 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, scale=0.0, out=None, status=None,
     if out is None:
         out = torch.empty((total_q, n_q, d), dtype=q.dtype, device=dev)
         _made_for(stream, out)
+    kind = q.dtype
+    strides = []
     for name, t, n, h in (("q", q, total_q, n_q), ("k", k, total_k, n_kv), ("v", v, total_k, n_kv)):
-        _require(tuple(t.shape) == (n, h, d) and t.dtype == q.dtype and t.device == dev and
-                 t.stride(2) == 1 and (h == 1 or t.stride(1) == d),
-                 f"{name}: [{n}, {h}, {d}] rows of q's type, contiguous within a token")
-    _require(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous() and out.device == dev,
+        st = t.stride()
+        if not (t.shape == (n, h, d) and t.dtype is kind and t.device == dev and st[2] == 1 and
+                (h == 1 or st[1] == d)):
+            raise ValueError(f"{name}: [{n}, {h}, {d}] rows of q's type, contiguous within a token")
+        strides.append(st[0] if n > 1 else h * d)
+    _require(out.shape == q.shape and out.dtype is kind and out.is_contiguous() and out.device == dev,
              "out: contiguous, of q's shape and type")
     batch = cu_q.numel() - 1
     cu_q_p = _ints(cu_q, batch + 1, "cu_q", dev, torch.int32)
@@ -528,9 +535,9 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, scale=0.0, out=None, status=None,
         cu_k_p = _ints(cu_k, batch + 1, "cu_k", dev, torch.int32)
     else:
         _require(total_k == total_q, "cu_k is needed where k has another length than q")
-    strides = [t.stride(0) if t.shape[0] > 1 else t.shape[1] * d for t in (q, k, v)]
-    _launch(_lib.tq_prompt_attention, "tq_prompt_attention", dev, stream, _ptr(q), _ptr(k), _ptr(v), _dtype_code16(q),
-            cu_q_p, cu_k_p, batch, total_q, total_k, n_q, n_kv, d, *strides, float(scale), _ptr(out), _ptr(status))
+    _launch(_lib.tq_prompt_attention, "tq_prompt_attention", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            _dtype_code16(q), cu_q_p, cu_k_p, batch, total_q, total_k, n_q, n_kv, d, *strides, float(scale),
+            out.data_ptr(), _ptr(status))
     return out
 
 
@@ -562,32 +569,26 @@ def tree_attention(rot, k_bits, v_bits, k_centroids, v_centroids, q, cu_nodes, l
     cu_p = _ints(cu_nodes, batch + 1, "cu_nodes", dev, torch.int32)
     lens_p = _ints(lens, batch, "lens", dev, torch.int32)
     _require(block_table.dim() == 2 and block_table.shape[0] == batch, "block_table: [batch, max_pages]")
-    table_p = _ints(block_table, batch * block_table.shape[1], "block_table", dev, torch.int32)
+    max_pages = block_table.shape[1]
+    table_p = _ints(block_table, batch * max_pages, "block_table", dev, torch.int32)
     n_pages, n_kv = pages["k_codes"].shape[:2]
-    for name, bits in (("k", k_bits), ("v", v_bits)):
-        c, n = pages[name + "_codes"], pages[name + "_norms"]
-        w = d * bits // 32                              # (the library refuses other blocks and widths)
-        _require(tuple(c.shape) == (n_pages, n_kv, page_size, w) and c.dtype == torch.int32 and
-                 c.is_contiguous() and c.device == dev,
-                 f"{name}_codes: int32 [{n_pages}, {n_kv}, {page_size}, {w}]")
-        _require(tuple(n.shape) == (n_pages, n_kv, page_size, d // 32) and n.dtype == torch.int16 and
-                 n.is_contiguous() and n.device == dev,
-                 f"{name}_norms: int16 [{n_pages}, {n_kv}, {page_size}, {d // 32}]")
+    # (the library refuses other blocks and widths)
+    storage = [_page_part(pages[name], name, kind, (n_pages, n_kv, page_size, w), dev)
+               for name, kind, w in (("k_codes", torch.int32, d * k_bits // 32), ("k_norms", torch.int16, d // 32),
+                                     ("v_codes", torch.int32, d * v_bits // 32), ("v_norms", torch.int16, d // 32))]
     words, mask_p = 0, None
     if tree_mask is not None:
         _require(tree_mask.dim() == 2, "tree_mask: [n_rows, words]")
         words = tree_mask.shape[1]
         mask_p = _ints(tree_mask, n_rows * words, "tree_mask", dev, torch.int64)
-    kc, kc_p = _host_floats(k_centroids)
-    vc, vc_p = _host_floats(v_centroids)
     if workspace is None:
         with _on(dev):
             need = tree_workspace_size(batch, n_rows, max_nodes, n_q, n_kv, max_len, d)
             workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
         _made_for(stream, workspace)
-    _launch(_lib.tq_tree_attention, "tq_tree_attention", dev, stream, rot.handle, k_bits, v_bits, block, kc_p,
-            vc_p, _ptr(q), _dtype_code16(q), cu_p, batch, n_rows, max_nodes, lens_p, max_len, mask_p, words,
-            n_q, n_kv, d, page_size, n_pages, table_p, block_table.shape[1], _ptr(pages["k_codes"]),
-            _ptr(pages["k_norms"]), _ptr(pages["v_codes"]), _ptr(pages["v_norms"]), float(scale), _ptr(out),
-            _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status))
+    _launch(_lib.tq_tree_attention, "tq_tree_attention", dev, stream, rot.handle, k_bits, v_bits, block,
+            _host_floats(k_centroids), _host_floats(v_centroids), q.data_ptr(), _dtype_code16(q), cu_p, batch,
+            n_rows, max_nodes, lens_p, max_len, mask_p, words, n_q, n_kv, d, page_size, n_pages, table_p, max_pages,
+            *storage, float(scale), out.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _ptr(status))
     return out
