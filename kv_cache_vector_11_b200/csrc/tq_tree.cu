@@ -462,13 +462,16 @@ __device__ __forceinline__ void unpack_block(const uint32_t * w, uint32_t nn, co
     }
 }
 
-// A row: NB blocks, one at a time (unrolled, the three widths are 30 KB of
-// instructions, more than stay close to the schedulers).
-template <int BITS, int NB>
+// A row: NB blocks, U of them to a pass of the loop.  One at a time the words move
+// down a register per block; unrolled, the three widths are 30 KB of instructions.
+// Beside one row tile that gains (16 trees over up to 32K tokens 133 -> 128 us, four
+// with d = 256 76 -> 75), beside two, whose softmax fills the rest of the cycles, it
+// loses (8 trees over 128K tokens 1.21 -> 1.34 ms).
+template <int BITS, int NB, int U>
 __device__ __forceinline__ void unpack_row(uint32_t * w, const uint32_t * norms, const uint32_t * tab, unsigned char * dst, int swz) {
     uint64_t n = norms[0];
     if constexpr (NB == 4) n |= (uint64_t)norms[1] << 32;
-#pragma unroll 1
+#pragma unroll U
     for (int blk = 0; blk < NB; ++blk) {
         unpack_block<BITS>(w, __byte_perm((uint32_t)n, 0u, 0x1010), tab, dst, blk, swz);
         n >>= 16;
@@ -903,9 +906,10 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                 break;
             }
             unsigned char * dst = smem + C::OFF_RING + s * C::BUF + r * 128;
-            if (bits == 4) unpack_row<4, NB>(w, norm, tab, dst, r & 7);
-            else if (bits == 3) unpack_row<3, NB>(w, norm, tab, dst, r & 7);
-            else unpack_row<2, NB>(w, norm, tab, dst, r & 7);
+            constexpr int U = MODE == PAIR ? 1 : NB;
+            if (bits == 4) unpack_row<4, NB, U>(w, norm, tab, dst, r & 7);
+            else if (bits == 3) unpack_row<3, NB, U>(w, norm, tab, dst, r & 7);
+            else unpack_row<2, NB, U>(w, norm, tab, dst, r & 7);
             tc::fence_proxy_async();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(full + 8u * s);
