@@ -1392,7 +1392,10 @@ constexpr int kTmThreads = 256;
 // memory, and the warps rotate the rows back.  R = 8 where few rows share a key
 // tile: their parts are many (one per warp of the grid that shared the tiles), so
 // more CTAs read them, eight reads of a thread at a time (rotation and
-// merge of 64 single tokens: 36 us with R = 32, 20 us with 8).
+// merge of 64 single tokens: 36 us with R = 32, 20 us with 8).  R = 8 also where
+// an SM gets no more than one such CTA (the call for 5 nodes of 8 heads, with the
+// dense rotation: 22.6 us with 32, 20.5 with 8); with more rows 32 is the faster
+// one (620 nodes of 16 heads, d = 256: 69 us against 72).
 template <int D, int R>
 __global__ void __launch_bounds__(kTmThreads) tree_combine_kernel(const __grid_constant__ TreeArgs a) {
     constexpr int E = D / 32, NW = kTmThreads / 32, GP = 32 / R, LD = D + 4, RW = R / NW;
@@ -1558,7 +1561,8 @@ int launch_tree(TreeArgs & a, cudaStream_t st) {
     } else if constexpr (D == 256) e = launch_tree_main<D, WIDE>(a, st);
     else e = a.streams == 2 ? launch_tree_main<D, STREAM>(a, st) : launch_tree_main<D, PAIR>(a, st);
     if (e) return e;
-    return a.rows_per_set == kFewRows ? launch_dependent(tree_combine_kernel<D, 8>, (unsigned)(a.own_rows / 8), kTmThreads, 0, st, a)
+    // (a.n_ctas: the SMs, or their warps)
+    return a.own_rows <= 8 * (int64_t)a.n_ctas || a.rows_per_set == kFewRows ? launch_dependent(tree_combine_kernel<D, 8>, (unsigned)(a.own_rows / 8), kTmThreads, 0, st, a)
                                       : launch_dependent(tree_combine_kernel<D, 32>, (unsigned)(a.own_rows / 32), kTmThreads, 0, st, a);
 }
 

@@ -445,6 +445,13 @@ def test_tree_pages_and_lengths(tq, page):
     _tree(tq, [1] * 12 + [0], lens, 4, 2, 128, 4, 3, page, chain=True)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["wht", "haar"])
+def test_tree_more_rows_than_one_merge_wave(tq, d, kind):
+    """1896 rows: merged 32 to a block, fewer than 8 rows an SM 8 to a block."""
+    _tree(tq, [200, 37], [400, 90], 8, 2, d, 4, 3, 32, kind=kind, pad=1)
+
+
 def test_tree_long_and_ragged(tq):
     _tree(tq, [4, 1, 30], [5000, 3, 1777], 4, 2, 128, 4, 3, 64)
     _tree(tq, [3], [20000], 2, 1, 64, 2, 2, 256)
