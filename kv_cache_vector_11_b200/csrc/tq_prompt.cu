@@ -152,8 +152,11 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     int * s_seq = reinterpret_cast<int *>(smem + C::OFF_MISC + 12);      // sequence, tile
     int * s_sums = reinterpret_cast<int *>(smem + C::OFF_MISC + 32);
 
-    // Barriers and TMEM first, beside the search for the tile.
-    if (tid == 0) {
+    const int ctrl = warp - 4 * NQ;                       // 0 and 3: MMAs, 1: copies, 2: value scan
+
+    // Barriers (by the thread that copies, which is the first to use them) and
+    // TMEM first, beside the search for the tile.
+    if (ctrl == 1 && lane == 0) {
         tc::mbar_init(q_full, 1);
         for (int i = 0; i < ST; ++i) {
             tc::mbar_init(full + 8u * i, 1);
@@ -175,7 +178,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         s_seq[0] = -1;
     }
     if (warp == 0) tc::tmem_alloc(sbase + (uint32_t)C::OFF_MISC, 512);
-    if (warp == 4 * NQ + 1 && lane < 3)
+    if (ctrl == 1 && lane < 3)
         asm volatile("prefetch.tensormap [%0];" :: "l"(lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap) : "memory");
 
     // Which sequence and tile: the tiles of all sequences are counted one sequence
@@ -266,44 +269,45 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     const int slots = NQ == 2 && i0 + a.queries < nq ? 2 : 1;
     const int h0 = hg * a.heads, hk = h0 / (a.n_q_heads / a.n_kv_heads);
 
+    // The copies into empty buffers start here, while the others meet.  Copy `it`:
+    // the buffers of a key tile, then of its values.
+    const int n_copies = 2 * NH * n;
+    int last = n_copies;                                  // copies that were started
+    auto copy_buffer = [&](int it) {
+        const int j = it / (2 * NH), h = it % NH, s = it % ST;
+        const CUtensorMap * map = (it / NH) % 2 == 0 ? &kmap : &vmap;
+        tc::mbar_arrive_expect_tx(full + 8u * s, (uint32_t)C::BUF);
+        for (int c = 0; c < SW; ++c)
+            tc::tma_load_3d(sbase + (uint32_t)(C::OFF_KV + s * C::BUF + c * C::SLICE), map, 64 * (h * SW + c), hk,
+                            k0 + (n - 1 - j) * kTile, full + 8u * s);
+    };
+    if (n > 0 && ctrl == 1 && lane == 0) {
+        // queries: boxes of 64 columns, GP heads, 128 / GP tokens
+        const uint32_t rows = (uint32_t)(a.heads * a.queries);
+        tc::mbar_arrive_expect_tx(q_full, (uint32_t)slots * (D / 64) * rows * 128u);
+        for (int i = 0; i < slots; ++i)
+            for (int c = 0; c < D / 64; ++c)
+                tc::tma_load_3d(sbase + (uint32_t)((i * (D / 64) + c) * C::SLICE), &qmap, 64 * c, h0,
+                                q0 + i0 + i * a.queries, q_full);
+        for (int it = 0; it < min(ST, n_copies); ++it) copy_buffer(it);
+    }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
-    const int ctrl = warp - 4 * NQ;                       // 0 and 3: MMAs, 1: copies, 2: value scan
 
     if (n > 0 && ctrl == 1) {
         if (lane == 0) {
-            // queries: boxes of 64 columns, GP heads, 128 / GP tokens
-            const uint32_t rows = (uint32_t)(a.heads * a.queries);
-            tc::mbar_arrive_expect_tx(q_full, (uint32_t)slots * (D / 64) * rows * 128u);
-            for (int i = 0; i < slots; ++i)
-                for (int c = 0; c < D / 64; ++c)
-                    tc::tma_load_3d(sbase + (uint32_t)((i * (D / 64) + c) * C::SLICE), &qmap, 64 * c, h0,
-                                    q0 + i0 + i * a.queries, q_full);
-            int it = 0;
             bool ok = true;
-            for (int j = 0; j < n && ok; ++j) {
-                const int key = k0 + (n - 1 - j) * kTile;
-#pragma unroll 1
-                for (int kv = 0; kv < 2 && ok; ++kv) {
-                    const CUtensorMap * map = kv == 0 ? &kmap : &vmap;
-#pragma unroll 1
-                    for (int h = 0; h < NH && ok; ++h, ++it) {
-                        const int s = it % ST;
-                        if (it >= ST) ok = fm::wait(empty + 8u * s, (uint32_t)((it / ST - 1) & 1));
-                        if (!ok) break;
-                        tc::mbar_arrive_expect_tx(full + 8u * s, (uint32_t)C::BUF);
-                        for (int c = 0; c < SW; ++c)
-                            tc::tma_load_3d(sbase + (uint32_t)(C::OFF_KV + s * C::BUF + c * C::SLICE), map,
-                                            64 * (h * SW + c), hk, key, full + 8u * s);
-                    }
-                }
+            for (int it = ST; it < n_copies && ok; ++it) {
+                ok = fm::wait(empty + 8u * (it % ST), (uint32_t)((it / ST - 1) & 1));
+                if (ok) copy_buffer(it);
+                else last = it;
             }
             if (!ok) *s_err = 1;
             // the last copy into every buffer lands before the CTA ends
             fm::wait(q_full, 0u);
-            for (int t = max(0, it - ST); t < it; ++t)
+            for (int t = max(0, last - ST); t < last; ++t)
                 fm::wait(full + 8u * (t % ST), (uint32_t)((t / ST) & 1));
         }
         __syncwarp();
