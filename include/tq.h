@@ -612,7 +612,8 @@ size_t tq_tree_workspace_size(int32_t batch, int32_t n_rows, int32_t max_nodes,
  * Block 32 with fp16 norms, default code order, keys without QJL signs.  The
  * rotated queries and the dequantized rows enter the products as fp16, sums are
  * fp32.  A cached token whose K or V norm is NaN or infinite makes the nodes that
- * attend it NaN, and no others.
+ * attend it NaN, and no others; a query row that is not finite makes its own output
+ * NaN.
  */
 tq_status tq_tree_attention(const tq_rotation * rot, int32_t k_bits, int32_t v_bits,
                             int32_t block, const float * k_centroids,

@@ -1456,7 +1456,9 @@ __global__ void __launch_bounds__(kTmThreads) tree_combine_kernel(const __grid_c
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (ml[u].x == -CUDART_INF_F) continue;      // no key attended (what its part holds is not read)
+            // No key attended: what its part holds is not read.  (A sum that is not 0
+            // beside -inf is that of NaN scores, which no maximum sees: it goes on.)
+            if (ml[u].x == -CUDART_INF_F && ml[u].y == 0.0f) continue;
             const float top = fmaxf(ref, ml[u].x);       // (a NaN stays in the sums)
             const float fa = ref == -CUDART_INF_F ? 0.0f : fm::ex2(ref - top), fb = fm::ex2(ml[u].x - top);
             ref = top;
