@@ -102,6 +102,7 @@ extern "C" {
 #define TQ_STATUS_TIMEOUT 4u   /* a bounded wait inside a kernel gave up */
 #define TQ_STATUS_NO_PAGES 8u  /* tq_page_tables could not place a request */
 #define TQ_STATUS_BAD_PAGE 16u /* a page or slot outside the page storage */
+#define TQ_STATUS_LIMIT 32u    /* lengths or offsets past the sizes that a call was made for */
 
 typedef enum tq_status {
     TQ_OK = 0,
@@ -595,10 +596,14 @@ size_t tq_tree_workspace_size(int32_t batch, int32_t n_rows, int32_t max_nodes,
  *               contiguous, 16-byte aligned.  Rows from cu_nodes[batch] on are
  *               padding: neither read nor written.
  *   cu_nodes:   device int32 [batch + 1], non-decreasing, from 0 to at most n_rows,
- *               at most max_nodes apart (1 <= max_nodes <= 256; nodes from
- *               max_nodes on are left out; offsets are clamped to [0, n_rows]).
+ *               at most max_nodes apart (1 <= max_nodes <= 256).  Offsets are
+ *               clamped to [0, n_rows]; rows of nodes from max_nodes on are neither
+ *               read nor written, while the nodes before them keep their places and
+ *               what they attend.
  *   lens:       device int32 [batch], 0 .. max_len (clamped); max_len <=
- *               max_pages * page_size, and below 2^31 - 255.
+ *               max_pages * page_size, and below 2^31 - 255.  Lengths and offsets
+ *               that exceed these limits (a captured call replayed with larger
+ *               ones, for instance) set TQ_STATUS_LIMIT.
  *   tree_mask:  device uint64 [n_rows][mask_words] or NULL; mask_words >=
  *               ceil(max_nodes / 64).
  *   block_table, page_size, n_pages, k_*, v_*: as in tq_decode_append_paged
@@ -608,7 +613,7 @@ size_t tq_tree_workspace_size(int32_t batch, int32_t n_rows, int32_t max_nodes,
  *   workspace:  >= tq_tree_workspace_size(...) bytes for these sizes, 256-byte
  *               aligned, needs no initialisation; calls that may overlap need one
  *               each.
- *   status_dev: device uint32 or NULL (TQ_STATUS_TIMEOUT).
+ *   status_dev: device uint32 or NULL (TQ_STATUS_TIMEOUT, TQ_STATUS_LIMIT).
  * Block 32 with fp16 norms, default code order, keys without QJL signs.  The
  * rotated queries and the dequantized rows enter the products as fp16, sums are
  * fp32.  A cached token whose K or V norm is NaN or infinite makes the nodes that

@@ -14,6 +14,7 @@ from ._lib import (  # noqa: F401
     FMT_NORM_F32,
     FORMAT_VERSION,
     STATUS_BAD_PAGE,
+    STATUS_LIMIT,
     STATUS_NO_PAGES,
     STATUS_NONFINITE,
     STATUS_NORM_SATURATED,

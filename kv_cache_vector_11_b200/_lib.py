@@ -21,6 +21,7 @@ STATUS_NONFINITE = 2
 STATUS_TIMEOUT = 4
 STATUS_NO_PAGES = 8
 STATUS_BAD_PAGE = 16
+STATUS_LIMIT = 32
 FMT_NORM_F32 = 1
 FMT_NORM_CORRECTED = 2
 FMT_GROUPED = 4
@@ -556,7 +557,11 @@ def tree_attention(rot, k_bits, v_bits, k_centroids, v_centroids, q, cu_nodes, l
     ``max_len``).  Node i attends all tokens before the nodes and the nodes
     whose bits are set in ``tree_mask`` (int64 [n_rows, words], 64 nodes to a
     word); without a mask the nodes 0 .. i.  ``pages`` and ``block_table`` as
-    in decode_append_paged.  Returns out, of q's type and shape."""
+    in decode_append_paged.  Returns out, of q's type and shape.
+
+    The lengths stay on the device, so the host does not see them exceed the
+    call's sizes: rows of nodes from ``max_nodes`` on are left as they were,
+    lengths are cut at ``max_len``, and STATUS_LIMIT is set in ``status``."""
     import torch
     n_rows, n_q, d = q.shape
     dev = q.device

@@ -102,16 +102,26 @@ struct TreeArgs {
     float2 * more_ml;
 };
 
-// Request b: its first row, nodes and cached tokens, clamped as the entry point says.
+// Request b: its first row, the nodes that are computed, the tokens before its
+// nodes (negative where some are not cached) and all its cached tokens, clamped as
+// the entry point says.  The nodes lie behind `ctx` also where max_nodes leaves
+// out the last of them.
 struct Request {
-    int32_t r0, n, len;
+    int32_t r0, n, ctx, len;
 };
 __device__ __forceinline__ Request request_of(const TreeArgs & a, int b) {
     Request q;
     q.r0 = min(max(a.cu[b], 0), a.n_rows);
-    q.n = min(min(max(a.cu[b + 1], q.r0), a.n_rows) - q.r0, a.max_nodes);
+    const int32_t nodes = min(max(a.cu[b + 1], q.r0), a.n_rows) - q.r0;
+    q.n = min(nodes, a.max_nodes);
     q.len = (int32_t)min((int64_t)max(a.lens[b], 0), a.max_len);
+    q.ctx = q.len - nodes;
     return q;
+}
+// Whether something of request b was clamped.
+__device__ __forceinline__ bool past_limits(const TreeArgs & a, int b) {
+    const int32_t r0 = a.cu[b], r1 = a.cu[b + 1], len = a.lens[b];
+    return r0 < 0 || r1 < r0 || r1 > a.n_rows || r1 - r0 > a.max_nodes || len < 0 || len > a.max_len;
 }
 __device__ __forceinline__ int sets_of(const TreeArgs & a, int n) {
     return (n * a.group + a.rows_per_set - 1) / a.rows_per_set;
@@ -328,6 +338,7 @@ __global__ void __launch_bounds__(kTpThreads) tree_prep_kernel(const __grid_cons
             if (b < a.batch) {
                 const Request q = request_of(a, b);
                 n = (int64_t)a.n_kv_heads * sets_of(a, q.n) * tiles_of(q.len);
+                if (a.status != nullptr && past_limits(a, b)) atomicOr(a.status, TQ_STATUS_LIMIT);
             }
             int64_t incl = n;
 #pragma unroll
@@ -947,7 +958,7 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
             const int node = in_req / a.group;
             const uint64_t * words = a.mask != nullptr && valid ? a.mask + (int64_t)(p.rq.r0 + node) * a.mask_words : nullptr;
             const float mul = valid ? a.q_mul[id] : 0.0f;
-            const int ctx0 = p.rq.len - p.rq.n;                        // tokens before the nodes
+            const int ctx0 = p.rq.ctx;                                 // tokens before the nodes
             const bool warp_valid = (MODE == PAIR ? w * kTile : 0) + (r & ~31) < p.rows;
             fm::RowState st{-CUDART_INF_F, 0.0f};
             bool first = true;
@@ -1217,7 +1228,7 @@ __global__ void __launch_bounds__(32 * FewCfg<D>::WARPS, 1) tree_few_kernel(cons
     Part p;
     while (it.next(a, p)) {
         const int t0 = p.tile0 * kTile, n_slabs = (min(p.rq.len - t0, p.tiles * kTile) + 15) >> 4;
-        const int ctx0 = p.rq.len - p.rq.n;
+        const int ctx0 = p.rq.ctx;
         // 16 tokens lie in one page, one behind the other; the page of the slab to
         // be fetched next was read a slab earlier
         int page = 0;

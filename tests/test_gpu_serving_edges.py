@@ -109,3 +109,60 @@ def test_prompt_nonfinite_queries_stay_in_their_rows(tq, d, value):
         hit[row, head] = True
     got = tq.prompt_attention(q, k, v, cu)
     assert bool(torch.isnan(got[hit]).all()) and torch.equal(got[~hit], want[~hit])
+
+
+# -- more nodes and tokens than the call allows for -------------------------------------------
+
+@pytest.mark.parametrize("kernel,limit", [("few", 3), ("few", 1), ("one tile", 8), ("one tile", 2), ("two tiles", 64),
+                                          ("two tiles", 17), ("wide", 5), ("wide", 1)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_tree_more_nodes_than_max_nodes(tq, kernel, limit, masked):
+    """Nodes from max_nodes on are left out; those kept attend what they attend in a
+    call that allows for all of them, and the status says that some were left out."""
+    n, hq, hk, d = KERNELS[kernel]
+    rng = np.random.default_rng(n + limit)
+    t = Tree(tq, [n, limit], [n + 80, limit + 3], hq, hk, d)
+    masks = [S.random_tree(rng, n), S.random_tree(rng, limit)]
+    mask = torch.from_numpy(S.mask_words(masks, -(-n // 64))).cuda() if masked else None
+    got, status = t.call(limit, mask=mask)
+    ref, absum, sq = t.reference(masks=masks if masked else None)
+    kept = np.r_[0:limit, n:n + limit]
+    g = f64(got)
+    assert np.all(np.linalg.norm(g - ref, axis=-1)[kept] <= S.tree_bound(ref, absum, sq, "bf16", d, max(t.lens))[kept])
+    assert np.all(g[limit:n] == 7.0), "rows of nodes that were left out were written"
+    assert status == tq.STATUS_LIMIT
+    assert t.call(n, mask=mask)[1] == 0
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_tree_limits_are_reported(tq, kernel):
+    n, hq, hk, d = KERNELS[kernel]
+    t = Tree(tq, [n, n], [n + 80, n + 3], hq, hk, d)
+    assert t.call(n)[1] == 0 and t.call(n, max_len=n + 82)[1] == 0
+    assert t.call(n, max_len=n + 79)[1] == tq.STATUS_LIMIT
+    for cu in ([-1, n, 2 * n], [0, n, 2 * n + 1], [0, n, n - 1]):
+        assert t.call(n, cu=cu)[1] == tq.STATUS_LIMIT
+    assert t.call(n, lens=[n + 80, -1])[1] == tq.STATUS_LIMIT
+    assert t.call(n, cu=[0, n, n])[1] == 0 and t.call(n, lens=[n + 80, 0])[1] == 0
+
+
+def test_tree_replayed_past_its_limits(tq):
+    """A captured step whose lengths outgrow what it was captured for says so."""
+    t = Tree(tq, [4, 4], [60, 64], 8, 2, 128)
+    cu, lens, status = i32([0, 4, 8]), i32([60, 64]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(tq.tree_workspace_size(2, 8, 4, 8, 2, 64, 128), dtype=torch.uint8, device="cuda")
+    out, table = torch.zeros_like(t.q), i32(t.table)
+
+    def call():
+        tq.tree_attention(t.rot, t.kb, t.vb, t.kc, t.vc, t.q, cu, lens, t.pages, table, t.page, 4, 64, out=out,
+                          workspace=ws, status=status)
+    call()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for new_cu, new_lens, past in (([0, 4, 8], [50, 10], False), ([0, 5, 8], [50, 10], True), ([0, 4, 8], [50, 65], True),
+                                   ([0, 3, 6], [64, 64], False)):
+        cu.copy_(i32(new_cu)), lens.copy_(i32(new_lens)), status.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(status) == (tq.STATUS_LIMIT if past else 0), (new_cu, new_lens)
