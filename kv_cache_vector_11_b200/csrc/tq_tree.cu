@@ -321,8 +321,9 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 
 // Block 0: the units before every request.  The others: one warp per (row,
 // head), q~ = R q times a power of two that brings the row's largest
-// coordinate into [1, 2), so that fp16 neither overflows nor loses the row;
-// q_mul carries the inverse, the softmax scale and log2 e.
+// coordinate into [1, 2) (from 2^127 on into [2, 4): the factor 2^-127 would be
+// subnormal, and its bits here those of 0), so that fp16 neither overflows nor
+// loses the row; q_mul carries the inverse, the softmax scale and log2 e.
 template <int D>
 __global__ void __launch_bounds__(kTpThreads) tree_prep_kernel(const __grid_constant__ TreeArgs a) {
     constexpr int E = D / 32, NW = kTpThreads / 32;
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(kTpThreads) tree_prep_kernel(const __grid_cons
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     int e = (int)(__float_as_uint(top) >> 23) - 127;
-    e = e == 128 ? 0 : max(e, -120);                     // (infinite or NaN rows stay so)
+    e = e == 128 ? 0 : min(max(e, -120), 126);           // (infinite or NaN rows stay so)
     const float f = __uint_as_float((uint32_t)(127 - e) << 23);
     const int hk = h / a.group, g = h - hk * a.group;
     const int64_t id = (int64_t)q.r0 * a.n_q_heads + (int64_t)hk * q.n * a.group + (int64_t)node * a.group + g;

@@ -166,3 +166,23 @@ def test_tree_replayed_past_its_limits(tq):
         g.replay()
         torch.cuda.synchronize()
         assert int(status) == (tq.STATUS_LIMIT if past else 0), (new_cu, new_lens)
+
+
+# -- magnitudes -------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_tree_rotated_queries_at_the_end_of_fp32(tq, kernel):
+    """Finite rows whose largest rotated coordinate lies in [2^127, 2^128) (dense
+    rotation: the Walsh-Hadamard sums would overflow)."""
+    n, hq, hk, d = KERNELS[kernel]
+    t = Tree(tq, [n], [n + 90], hq, hk, d, kind="haar", dtype=torch.float32)
+    rng = np.random.default_rng(d)
+    y = rng.standard_normal((t.rows, hq, d)) * 2.0**120
+    y[..., d // 3] = 1.5 * 2.0**127
+    q = torch.from_numpy((y @ P.oracle_rotation("haar", d, W.SEED_ROT)).astype(np.float32)).cuda()
+    scale = float(np.float32(0.1 * 2.0**-126))
+    assert bool(torch.isfinite(q).all()) and scale > 0
+    got, status = t.call(n, q=q, scale=scale)
+    ref, absum, sq = t.reference(q=q, scale=scale)
+    assert status == 0
+    assert np.all(np.linalg.norm(f64(got) - ref, axis=-1) <= S.tree_bound(ref, absum, sq, "f32", d, max(t.lens)))
