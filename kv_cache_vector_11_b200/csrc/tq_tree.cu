@@ -406,7 +406,9 @@ __global__ void __launch_bounds__(kTpThreads) tree_prep_kernel(const __grid_cons
 #pragma unroll
     for (int k = 0; k < E; ++k) v[k] *= f;
     store_vec<E>(a.q_rows, TQ_DTYPE_F16, id * D + E * lane, v);
-    if (lane == 0) a.q_mul[id] = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
+    // (not 0, which times the -inf of a masked key is NaN; products with the
+    // smallest normal number are below 2^-90 as well)
+    if (lane == 0) a.q_mul[id] = fmaxf(a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23), 0x1p-126f);
 }
 
 // ---------------------------------------------------------------------------

@@ -186,3 +186,16 @@ def test_tree_rotated_queries_at_the_end_of_fp32(tq, kernel):
     ref, absum, sq = t.reference(q=q, scale=scale)
     assert status == 0
     assert np.all(np.linalg.norm(f64(got) - ref, axis=-1) <= S.tree_bound(ref, absum, sq, "f32", d, max(t.lens)))
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_tree_zero_queries_with_a_small_scale(tq, kernel):
+    """Scores of 0 at a scale whose product with a row's factor would underflow: the
+    mean of the values that the row attends."""
+    n, hq, hk, d = KERNELS[kernel]
+    t = Tree(tq, [n], [n + 90], hq, hk, d, dtype=torch.float32)
+    t.q.zero_()
+    got, status = t.call(n, scale=1e-10)
+    ref, absum, sq = t.reference(scale=1e-10)
+    assert status == 0
+    assert np.all(np.linalg.norm(f64(got) - ref, axis=-1) <= S.tree_bound(ref, absum, sq, "f32", d, max(t.lens)))
