@@ -116,7 +116,10 @@ __device__ __noinline__ void prompt_row(const PromptArgs & a, int64_t tok, int h
         for (int e = 0; e < E; ++e) s = fmaf(q[e], to_f32(kp[lane + 32 * e]), s);
         for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
         const float mn = fmaxf(m, s);
-        const float c = m == -CUDART_INF_F ? 0.0f : expf(m - mn), p = expf(s - mn);
+        // (a score of -inf has weight 0, also in front of the first finite one; a
+        // row with no other divides 0 by 0)
+        const float c = m == -CUDART_INF_F ? 0.0f : expf(m - mn);
+        const float p = s == -CUDART_INF_F && mn == s ? 0.0f : expf(s - mn);
         m = mn;
         l = l * c + p;
         for (int e = 0; e < E; ++e) o[e] = o[e] * c + p * to_f32(vp[lane + 32 * e]);

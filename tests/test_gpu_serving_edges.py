@@ -111,6 +111,29 @@ def test_prompt_nonfinite_queries_stay_in_their_rows(tq, d, value):
     assert bool(torch.isnan(got[hit]).all()) and torch.equal(got[~hit], want[~hit])
 
 
+# -- prompt keys whose score is -infinity -----------------------------------------------------
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("far", [False, True])
+def test_prompt_first_score_minus_infinity(tq, d, far):
+    """A key with a score of -infinity has weight 0, also where a value that is not
+    finite, at a key that the row does not attend, has the rows computed on the CUDA cores."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    n = 150
+    q, k, v = (torch.randn((n, h, d), generator=g, device="cuda").bfloat16() for h in (2, 1, 1))
+    q[..., 0] = q[..., 0].abs() + 0.5
+    k[0, 0, 0] = float("-inf")
+    if far:
+        v[100, 0, 3] = float("nan")
+    got = f64(tq.prompt_attention(q, k, v, i32([0, n])))
+    seen = 100 if far else n
+    ref, absum, sq = osv.prompt_attention(f64(q)[1:seen], f64(k)[1:seen], f64(v)[1:seen], [0, seen - 1], [0, seen - 1])
+    assert np.isnan(got[0]).all()                             # attends nothing else
+    assert np.isfinite(got[1:seen]).all(), "a weight of 0 made a row NaN"
+    assert np.all(np.abs(got[1:seen] - ref) <= S.prompt_bound(ref, absum, sq, "bf16", d, n))
+    assert not far or np.isnan(got[100:, :, 3]).all() and np.isfinite(got[100:, :, 4:]).all()
+
+
 # -- more nodes and tokens than the call allows for -------------------------------------------
 
 @pytest.mark.parametrize("kernel,limit", [("few", 3), ("few", 1), ("one tile", 8), ("one tile", 2), ("two tiles", 64),
