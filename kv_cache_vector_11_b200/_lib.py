@@ -407,10 +407,14 @@ def _page_part(t, name, kind, shape, device):
     return t.data_ptr()
 
 
-def _host_floats(x):
-    """x as fp32 in a bytes object, which ctypes passes as a pointer (0.3 us; an
-    array's address by ``ndarray.ctypes`` takes several times that)."""
-    return np.ascontiguousarray(x, dtype=np.float32).tobytes()
+def _host_floats(x, n, name):
+    """The n values of x as fp32 in a bytes object, which ctypes passes as a
+    pointer (0.3 us; an array's address by ``ndarray.ctypes`` takes several times
+    that).  The library reads n of them whatever x holds."""
+    b = np.ascontiguousarray(x, dtype=np.float32).tobytes()
+    if len(b) != 4 * n:
+        raise ValueError(f"{name}: {n} values, not {len(b) // 4}")
+    return b
 
 
 def _stream_of(device):
@@ -501,7 +505,8 @@ def quantize_kv_paged(rot, bits, centroids, boundaries, x, slots, codes, norms, 
     codes_p = _page_part(codes, "codes", torch.int32, (n_pages, heads, page_size, w), dev)
     norms_p = _page_part(norms, "norms", torch.int16, (n_pages, heads, page_size, d // 32), dev)
     _launch(_lib.tq_quantize_kv_paged, "tq_quantize_kv_paged", dev, stream, rot.handle, bits, block,
-            _host_floats(centroids), _host_floats(boundaries), x.data_ptr(), _dtype_code(x), n, heads, d,
+            _host_floats(centroids, 1 << bits, "centroids"), _host_floats(boundaries, (1 << bits) - 1, "boundaries"),
+            x.data_ptr(), _dtype_code(x), n, heads, d,
             slots_p, page_size, n_pages, codes_p, norms_p, _ptr(status))
 
 
@@ -592,8 +597,8 @@ def tree_attention(rot, k_bits, v_bits, k_centroids, v_centroids, q, cu_nodes, l
             workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
         _made_for(stream, workspace)
     _launch(_lib.tq_tree_attention, "tq_tree_attention", dev, stream, rot.handle, k_bits, v_bits, block,
-            _host_floats(k_centroids), _host_floats(v_centroids), q.data_ptr(), _dtype_code16(q), cu_p, batch,
-            n_rows, max_nodes, lens_p, max_len, mask_p, words, n_q, n_kv, d, page_size, n_pages, table_p, max_pages,
+            _host_floats(k_centroids, 1 << k_bits, "k_centroids"), _host_floats(v_centroids, 1 << v_bits, "v_centroids"),
+            q.data_ptr(), _dtype_code16(q), cu_p, batch, n_rows, max_nodes, lens_p, max_len, mask_p, words, n_q, n_kv, d, page_size, n_pages, table_p, max_pages,
             *storage, float(scale), out.data_ptr(), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), _ptr(status))
     return out

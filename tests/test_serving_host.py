@@ -161,3 +161,40 @@ def test_python_refuses_misread_tensors(rot):
         with pytest.raises(ValueError):
             tq.tree_attention(rot, 4, 3, kc, tq.build_codebook(3)[0], kw["q"], kw["cu"], kw["lens"], kw["pages"],
                               kw["table"], 16, 2, 64, tree_mask=kw["mask"])
+
+
+def _quantize_call(rot, bits, c, t, **kw):
+    x = torch.zeros((4, 2, 128), dtype=torch.bfloat16)
+    codes, norms = _i32(3, 2, 16, 4 * bits), torch.zeros((3, 2, 16, 4), dtype=torch.int16)
+    tq.quantize_kv_paged(rot, bits, c, t, x, torch.zeros(4, dtype=torch.int64), codes, norms, 16, **kw)
+
+
+def _tree_call(rot, kb, vb, kc, vc, **kw):
+    norms = torch.zeros((3, 2, 16, 4), dtype=torch.int16)
+    pages = dict(k_codes=_i32(3, 2, 16, 4 * kb), k_norms=norms, v_codes=_i32(3, 2, 16, 4 * vb), v_norms=norms)
+    q = torch.zeros((4, 4, 128), dtype=torch.bfloat16)
+    kw.setdefault("workspace", torch.zeros(256, dtype=torch.uint8))
+    tq.tree_attention(rot, kb, vb, kc, vc, q, _i32(3), _i32(2), pages, _i32(2, 4), 16, 2, 64, **kw)
+
+
+def test_python_refuses_codebooks_of_another_width(rot):
+    """The library reads 2^bits centroids and 2^bits - 1 boundaries; a shorter array
+    is refused (tensors on the CPU are too, but by another message)."""
+    books = {b: tq.build_codebook(b) for b in (2, 3, 4)}
+    for bits in (2, 3, 4):
+        c, t = books[bits]
+        for other in books:
+            if other == bits:
+                continue
+            with pytest.raises(ValueError, match="centroids"):
+                _quantize_call(rot, bits, books[other][0], t)
+            with pytest.raises(ValueError, match="boundaries"):
+                _quantize_call(rot, bits, c, books[other][1])
+            with pytest.raises(ValueError, match="k_centroids"):
+                _tree_call(rot, bits, 3, books[other][0], books[3][0])
+            with pytest.raises(ValueError, match="v_centroids"):
+                _tree_call(rot, 4, bits, books[4][0], books[other][0])
+        with pytest.raises(ValueError, match="not on a CUDA device"):
+            _quantize_call(rot, bits, c, t)
+        with pytest.raises(ValueError, match="not on a CUDA device"):
+            _tree_call(rot, bits, bits, list(c), c.astype(np.float64))
