@@ -400,6 +400,16 @@ def _ints(t, n, name, device, kind):
     return t.data_ptr()
 
 
+def _status_ptr(t, device):
+    """Pointer of the status word (None: none is kept)."""
+    import torch
+    if t is None:
+        return None
+    if not (t.device == device and t.dtype in (torch.int32, torch.uint32) and t.numel() > 0):
+        raise ValueError(f"status: int32 of at least one entry on {device}")
+    return t.data_ptr()
+
+
 def _page_part(t, name, kind, shape, device):
     """Pointer of one array of the page storage, [page][kv head][token][..]."""
     if not (t.shape == shape and t.dtype is kind and t.is_contiguous() and t.device == device):
@@ -483,7 +493,7 @@ def page_tables(ctx_lens, new_lens, page_size, n_pages, free_pages, block_table,
             _ints(out["total_lens"], batch, "total_lens", dev, i32),
             _ints(out["slots"], n_slots, "slots", dev, torch.int64),
             None if positions is None else _ints(positions, n_slots, "positions", dev, i32), n_slots,
-            _ints(out["n_taken"], 1, "n_taken", dev, i32), _ptr(status))
+            _ints(out["n_taken"], 1, "n_taken", dev, i32), _status_ptr(status, dev))
     _launch(_lib.tq_page_tables, "tq_page_tables", dev, stream, *args)
     return out
 
@@ -507,7 +517,7 @@ def quantize_kv_paged(rot, bits, centroids, boundaries, x, slots, codes, norms, 
     _launch(_lib.tq_quantize_kv_paged, "tq_quantize_kv_paged", dev, stream, rot.handle, bits, block,
             _host_floats(centroids, 1 << bits, "centroids"), _host_floats(boundaries, (1 << bits) - 1, "boundaries"),
             x.data_ptr(), _dtype_code(x), n, heads, d,
-            slots_p, page_size, n_pages, codes_p, norms_p, _ptr(status))
+            slots_p, page_size, n_pages, codes_p, norms_p, _status_ptr(status, dev))
 
 
 def prompt_attention(q, k, v, cu_q, cu_k=None, scale=0.0, out=None, status=None, stream=None):
@@ -543,7 +553,7 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, scale=0.0, out=None, status=None,
         _require(total_k == total_q, "cu_k is needed where k has another length than q")
     _launch(_lib.tq_prompt_attention, "tq_prompt_attention", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
             _dtype_code16(q), cu_q_p, cu_k_p, batch, total_q, total_k, n_q, n_kv, d, *strides, float(scale),
-            out.data_ptr(), _ptr(status))
+            out.data_ptr(), _status_ptr(status, dev))
     return out
 
 
@@ -596,9 +606,10 @@ def tree_attention(rot, k_bits, v_bits, k_centroids, v_centroids, q, cu_nodes, l
             need = tree_workspace_size(batch, n_rows, max_nodes, n_q, n_kv, max_len, d)
             workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
         _made_for(stream, workspace)
+    _require(workspace.device == dev and workspace.is_contiguous(), "workspace: contiguous, on q's device")
     _launch(_lib.tq_tree_attention, "tq_tree_attention", dev, stream, rot.handle, k_bits, v_bits, block,
             _host_floats(k_centroids, 1 << k_bits, "k_centroids"), _host_floats(v_centroids, 1 << v_bits, "v_centroids"),
             q.data_ptr(), _dtype_code16(q), cu_p, batch, n_rows, max_nodes, lens_p, max_len, mask_p, words, n_q, n_kv, d, page_size, n_pages, table_p, max_pages,
             *storage, float(scale), out.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _ptr(status))
+            workspace.numel() * workspace.element_size(), _status_ptr(status, dev))
     return out

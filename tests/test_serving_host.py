@@ -198,3 +198,25 @@ def test_python_refuses_codebooks_of_another_width(rot):
             _quantize_call(rot, bits, c, t)
         with pytest.raises(ValueError, match="not on a CUDA device"):
             _tree_call(rot, bits, bits, list(c), c.astype(np.float64))
+
+
+@pytest.mark.parametrize("status", [torch.zeros(1, dtype=torch.int32, device="meta"), torch.zeros(1, dtype=torch.int64),
+                                    torch.zeros(1), torch.zeros(0, dtype=torch.int32)])
+def test_python_refuses_a_status_that_the_kernels_cannot_write(rot, status):
+    """A status word on another device would be a write to an address of that device."""
+    (kc, kt), (vc, _) = tq.build_codebook(4), tq.build_codebook(3)
+    q = torch.zeros((4, 2, 128), dtype=torch.bfloat16)
+    for call in (lambda: tq.page_tables(_i32(2), _i32(2), 16, 4, _i32(4), _i32(2, 2), 8, status=status),
+                 lambda: _quantize_call(rot, 4, kc, kt, status=status),
+                 lambda: tq.prompt_attention(q, q, q, _i32(3), status=status),
+                 lambda: _tree_call(rot, 4, 3, kc, vc, status=status)):
+        with pytest.raises(ValueError, match="status"):
+            call()
+
+
+@pytest.mark.parametrize("workspace", [torch.zeros(1 << 20, dtype=torch.uint8, device="meta"),
+                                       torch.zeros(1 << 20, dtype=torch.uint8)[::2]])
+def test_python_refuses_a_workspace_on_another_device(rot, workspace):
+    kc, vc = tq.build_codebook(4)[0], tq.build_codebook(3)[0]
+    with pytest.raises(ValueError, match="workspace"):
+        _tree_call(rot, 4, 3, kc, vc, workspace=workspace)
