@@ -435,14 +435,20 @@ def _stream_of(device):
     return raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
-def _made_for(stream, *tensors):
-    """Tensors that a call allocated (on the current stream) and hands to a
-    launch on ``stream``: their memory is not given out again before that
-    stream is done with them."""
-    if stream is not None:
-        for t in tensors:
-            if t.is_cuda:
-                t.record_stream(stream)
+def _empty(shape, dtype, device, stream, returned=True):
+    """Memory that a call on ``stream`` allocates itself.  It comes from that
+    stream's own blocks: one that the current stream gave back may still be read
+    or written there, by work which ``stream`` does not wait for.  What the call
+    returns is used on the current stream, and not given out again before that
+    stream is done with it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _launch(fn, where, device, stream, *args):
@@ -476,12 +482,11 @@ def page_tables(ctx_lens, new_lens, page_size, n_pages, free_pages, block_table,
     dev = ctx_lens.device
     batch = ctx_lens.shape[0]
     if out is None:
-        out = {"cu_new": torch.empty((batch + 1,), dtype=torch.int32, device=dev),
-               "total_lens": torch.empty((batch,), dtype=torch.int32, device=dev),
-               "slots": torch.empty((n_slots,), dtype=torch.int64, device=dev),
-               "positions": torch.empty((n_slots,), dtype=torch.int32, device=dev),
-               "n_taken": torch.empty((1,), dtype=torch.int32, device=dev)}
-        _made_for(stream, *out.values())
+        out = {"cu_new": _empty((batch + 1,), torch.int32, dev, stream),
+               "total_lens": _empty((batch,), torch.int32, dev, stream),
+               "slots": _empty((n_slots,), torch.int64, dev, stream),
+               "positions": _empty((n_slots,), torch.int32, dev, stream),
+               "n_taken": _empty((1,), torch.int32, dev, stream)}
     i32 = torch.int32
     _require(block_table.dim() == 2 and block_table.shape[0] == batch, "block_table: [batch, max_pages]")
     n_free, max_pages = free_pages.numel(), block_table.shape[1]
@@ -532,8 +537,7 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, scale=0.0, out=None, status=None,
     total_k, n_kv, _ = k.shape
     dev = q.device
     if out is None:
-        out = torch.empty((total_q, n_q, d), dtype=q.dtype, device=dev)
-        _made_for(stream, out)
+        out = _empty((total_q, n_q, d), q.dtype, dev, stream)
     kind = q.dtype
     strides = []
     for name, t, n, h in (("q", q, total_q, n_q), ("k", k, total_k, n_kv), ("v", v, total_k, n_kv)):
@@ -582,8 +586,7 @@ def tree_attention(rot, k_bits, v_bits, k_centroids, v_centroids, q, cu_nodes, l
     dev = q.device
     batch = lens.shape[0]
     if out is None:
-        out = torch.empty((n_rows, n_q, d), dtype=q.dtype, device=dev)
-        _made_for(stream, out)
+        out = _empty((n_rows, n_q, d), q.dtype, dev, stream)
     _require(q.is_contiguous() and out.shape == q.shape and out.dtype == q.dtype and
              out.is_contiguous() and out.device == dev, "q and out: contiguous, same shape and type")
     cu_p = _ints(cu_nodes, batch + 1, "cu_nodes", dev, torch.int32)
@@ -604,12 +607,11 @@ def tree_attention(rot, k_bits, v_bits, k_centroids, v_centroids, q, cu_nodes, l
     if workspace is None:
         with _on(dev):
             need = tree_workspace_size(batch, n_rows, max_nodes, n_q, n_kv, max_len, d)
-            workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
-        _made_for(stream, workspace)
+        workspace = _empty((max(need, 256),), torch.uint8, dev, stream, returned=False)
     _require(workspace.device == dev and workspace.is_contiguous(), "workspace: contiguous, on q's device")
     _launch(_lib.tq_tree_attention, "tq_tree_attention", dev, stream, rot.handle, k_bits, v_bits, block,
             _host_floats(k_centroids, 1 << k_bits, "k_centroids"), _host_floats(v_centroids, 1 << v_bits, "v_centroids"),
-            q.data_ptr(), _dtype_code16(q), cu_p, batch, n_rows, max_nodes, lens_p, max_len, mask_p, words, n_q, n_kv, d, page_size, n_pages, table_p, max_pages,
-            *storage, float(scale), out.data_ptr(), workspace.data_ptr(),
+            q.data_ptr(), _dtype_code16(q), cu_p, batch, n_rows, max_nodes, lens_p, max_len, mask_p, words, n_q, n_kv, d,
+            page_size, n_pages, table_p, max_pages, *storage, float(scale), out.data_ptr(), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), _status_ptr(status, dev))
     return out

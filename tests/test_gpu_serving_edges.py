@@ -222,3 +222,73 @@ def test_tree_zero_queries_with_a_small_scale(tq, kernel):
     ref, absum, sq = t.reference(scale=1e-10)
     assert status == 0
     assert np.all(np.linalg.norm(f64(got) - ref, axis=-1) <= S.tree_bound(ref, absum, sq, "f32", d, max(t.lens)))
+
+
+# -- calls on another stream ------------------------------------------------------------------
+
+def _busy(x, n=20):
+    for _ in range(n):
+        x = x @ x * 1e-2
+    return x
+
+
+def _stream_calls(tq):
+    """The calls that allocate what they are not given, each with the size in bytes
+    of what it allocates: name -> (call(stream), sizes)."""
+    t = Tree(tq, [40, 20], [2000, 700], 8, 2, 128, page=32)
+    q, k = (torch.randn((900, h, 128), device="cuda").bfloat16() for h in (8, 2))
+    cu_t, lens, table, cu_p = i32(t.cu), i32(t.lens), i32(t.table), i32([0, 800, 900])
+    need = tq.tree_workspace_size(2, 60, 40, 8, 2, 2000, 128)
+    free, new = i32(np.arange(400)), i32([3000, 2000])
+    zero, tab = i32([0, 0]), i32(np.full((2, 200), -1))
+
+    def tree(stream):
+        return [tq.tree_attention(t.rot, t.kb, t.vb, t.kc, t.vc, t.q, cu_t, lens, t.pages, table, 32, 40, 2000,
+                                  stream=stream)]
+
+    def prompt(stream):
+        return [tq.prompt_attention(q, k, k, cu_p, stream=stream)]
+
+    def tables(stream):
+        return list(tq.page_tables(zero, new, 16, 400, free, tab, 5000, stream=stream).values())
+    return {"tree": (tree, [need, 2 * t.q.numel()]), "prompt": (prompt, [2 * q.numel()]),
+            "tables": (tables, [40000, 20000, 12, 8, 4])}
+
+
+@pytest.mark.parametrize("which", ["tree", "prompt", "tables"])
+def test_memory_of_a_call_is_not_in_use_on_the_current_stream(tq, which):
+    """stream= another than the current one, outputs and workspace left to the call:
+    blocks that the current stream gave back, with work on them still queued there,
+    are not among what the call writes."""
+    call, sizes = _stream_calls(tq)[which]
+    want = call(None)
+    side, x = torch.cuda.Stream(), torch.randn((4096, 4096), device="cuda")
+    torch.cuda.synchronize()
+    before = [torch.full((n,), 0x3C, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+    _busy(x)
+    copies = [t.clone() for t in before]              # queued behind the products
+    del before
+    got = call(side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(bool((t == 0x3C).all()) for t in copies)
+
+
+@pytest.mark.parametrize("which", ["tree", "prompt", "tables"])
+def test_outputs_of_a_call_are_kept_for_the_current_stream(tq, which):
+    """The same outputs, given back while the current stream has still to read them,
+    are not among what a later call on that stream writes."""
+    call, _ = _stream_calls(tq)[which]
+    want = call(None)
+    side, x = torch.cuda.Stream(), torch.randn((4096, 4096), device="cuda")
+    torch.cuda.synchronize()
+    got = call(side)
+    torch.cuda.current_stream().wait_stream(side)
+    _busy(x)
+    copies = [t.clone() for t in got]
+    sizes = [t.numel() * t.element_size() for t in got]
+    del got
+    with torch.cuda.stream(side):
+        later = [torch.full((n,), 0x3C, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(copies, want)) and len(later) == 3 * len(sizes)
