@@ -147,6 +147,11 @@ __device__ __forceinline__ int64_t part_at(int64_t row, int col) {
     return ((row >> 5) * (D / 4) + (col >> 2)) * 128 + (row & 31) * 4;
 }
 
+// Reference and sum of a part.  A reference of -inf says that no key was attended
+// and the sums are not to be read; NaN scores, which no maximum sees, leave one
+// beside a NaN sum, and must be.
+__device__ __forceinline__ float2 part_ml(float ref, float sum) { return make_float2(isnan(sum) ? sum : ref, sum); }
+
 // The parts of this CTA's range, one per (request, KV head, row set).
 struct Part {
     int b, hk, set, tile0, tiles;    // key tiles [tile0, tile0 + tiles)
@@ -1025,7 +1030,7 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                             *reinterpret_cast<uint4 *>(dst + part_at<D>(part_row, c + x)) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
                     }
                 }
-                if (valid) *ml = make_float2(st.ref, st.sum);
+                if (valid) *ml = part_ml(st.ref, st.sum);
             }
             tc::fence_before_sync();
             tc::mbar_arrive(o_free + 8u * w);
@@ -1386,7 +1391,7 @@ __global__ void __launch_bounds__(32 * FewCfg<D>::WARPS, 1) tree_few_kernel(cons
             const int r = 2 * t + c;
             if (r >= p.rows) continue;
             const int64_t at = own ? p.row_id + r : (int64_t)worker * a.more_rows + r;
-            if (g == 0) (own ? a.own_ml : a.more_ml)[at] = make_float2(ref[c], total);
+            if (g == 0) (own ? a.own_ml : a.more_ml)[at] = part_ml(ref[c], total);
 #pragma unroll
             for (int b = 0; b < NB; ++b)
                 *reinterpret_cast<float4 *>(parts + part_at<D>(at, 32 * b + 4 * g)) =
@@ -1470,9 +1475,7 @@ __global__ void __launch_bounds__(kTmThreads) tree_combine_kernel(const __grid_c
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            // No key attended: what its part holds is not read.  (A sum that is not 0
-            // beside -inf is that of NaN scores, which no maximum sees: it goes on.)
-            if (ml[u].x == -CUDART_INF_F && ml[u].y == 0.0f) continue;
+            if (ml[u].x == -CUDART_INF_F) continue;      // no key attended (what its part holds is not read)
             const float top = fmaxf(ref, ml[u].x);       // (a NaN stays in the sums)
             const float fa = ref == -CUDART_INF_F ? 0.0f : fm::ex2(ref - top), fb = fm::ex2(ml[u].x - top);
             ref = top;
