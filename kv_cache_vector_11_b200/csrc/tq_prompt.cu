@@ -528,7 +528,10 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     auto scale_acc = [&](float f) {
                         bool r = j == 0 || fm::wait(o_done + 8u * (2 * i + 1), (uint32_t)((j - 1) & 1));
                         if (g == 1) r = r && fm::wait(o_done + 8u * (2 * i), (uint32_t)(j & 1));
-                        scale_row<D>(o_tm, f);
+                        // (the accumulator's loads and stores want a converged warp, and the
+                        // votes that follow the same answer in all its lanes)
+                        r = __all_sync(0xffffffffu, r);
+                        if (r) scale_row<D>(o_tm, f);
                         return r;
                     };
                     const uint32_t half = s_tm + (uint32_t)g * fm::kHalfCols;

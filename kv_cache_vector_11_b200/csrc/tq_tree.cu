@@ -987,8 +987,8 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
 #pragma unroll 1
                 for (int g = 0; g < 2; ++g) {
                     // (the scores that follow in this half wait for these weights)
-                    ok = fm::wait(s_full + 8u * (2 * slot + g), use & 1u);
-                    ok = __all_sync(0xffffffffu, ok);
+                    const bool scored = fm::wait(s_full + 8u * (2 * slot + g), use & 1u);
+                    ok = __all_sync(0xffffffffu, ok && scored);
                     if (!ok) break;
                     tc::fence_after_sync();
                     if (warp_valid) {
@@ -998,6 +998,9 @@ __global__ void __launch_bounds__(TaCfg<D, MODE>::THREADS, 1) tree_kernel(const 
                         auto scale_acc = [&](float f) {
                             bool r = first || fm::wait(o_done + 8u * (2 * w + 1), (uint32_t)((mine - 1) & 1));
                             if (g == 1) r = r && fm::wait(o_done + 8u * (2 * w), (uint32_t)(mine & 1));
+                            // (the accumulator's loads and stores want a converged warp, and the
+                            // votes that follow the same answer in all its lanes)
+                            r = __all_sync(0xffffffffu, r);
                             fm::rescale(o_tm, D, f);
                             return r;
                         };
