@@ -220,3 +220,75 @@ def test_python_refuses_a_workspace_on_another_device(rot, workspace):
     kc, vc = tq.build_codebook(4)[0], tq.build_codebook(3)[0]
     with pytest.raises(ValueError, match="workspace"):
         _tree_call(rot, 4, 3, kc, vc, workspace=workspace)
+
+
+def test_python_refusals_name_the_tensor(rot):
+    """What test_python_refuses_misread_tensors refuses, by message: tensors on the CPU
+    raise ValueError at the latest, whatever else is wrong with them."""
+    q, k = (torch.zeros((4, h, 128), dtype=torch.bfloat16) for h in (4, 2))
+    cu = _i32(3)
+
+    def refused(match, call, **bad):
+        with pytest.raises(ValueError, match=match):
+            call(**bad)
+
+    def prompt_(q=q, k=k, v=k, cu_q=cu, **kw):
+        tq.prompt_attention(q, k, v, cu_q, **kw)
+    refused("not on a CUDA device", prompt_)
+    refused("^cu_q:", prompt_, cu_q=cu.long())
+    refused("^cu_q:", prompt_, cu_q=_i32(6)[::2])
+    refused("^k:", prompt_, q=q.half())
+    refused("^q:", prompt_, q=torch.zeros((4, 128, 4), dtype=torch.bfloat16).transpose(1, 2))
+    refused("^k:", prompt_, k=k[:, :, ::2])
+    refused("^v:", prompt_, v=k[:3])
+    refused("^v:", prompt_, v=q)
+    refused("^cu_k:", prompt_, cu_k=_i32(4))
+    refused("^out:", prompt_, out=q.float())
+    refused("^out:", prompt_, out=q.transpose(0, 1).contiguous().transpose(0, 1))
+    refused("^cu_k is needed", prompt_, k=torch.zeros((5, 2, 128), dtype=torch.bfloat16),
+            v=torch.zeros((5, 2, 128), dtype=torch.bfloat16))
+
+    def tables_(ctx=_i32(2), new=_i32(2), free=_i32(4), table=_i32(2, 2), n_slots=8, **kw):
+        tq.page_tables(ctx, new, 16, 4, free, table, n_slots, **kw)
+    out = dict(cu_new=_i32(3), total_lens=_i32(2), slots=torch.zeros(8, dtype=torch.int64), positions=_i32(8), n_taken=_i32(1))
+    refused("not on a CUDA device", tables_)
+    refused("not on a CUDA device", tables_, out=out)
+    refused("^ctx_lens:", tables_, ctx=_i32(2).long())
+    refused("^new_lens:", tables_, new=_i32(3))
+    refused("^free_pages:", tables_, free=_i32(8)[::2])
+    refused("^block_table:", tables_, table=_i32(3, 2))
+    refused("^block_table:", tables_, table=_i32(2, 4)[:, ::2])
+    for name, wrong in (("cu_new", _i32(2)), ("total_lens", _i32(3)), ("slots", _i32(8)), ("positions", _i32(7)),
+                        ("n_taken", torch.zeros(1))):
+        refused(f"^{name}:", tables_, out=dict(out, **{name: wrong}))
+
+    (kc, kt), vc = tq.build_codebook(4), tq.build_codebook(3)[0]
+    slots, codes, norms = torch.zeros(4, dtype=torch.int64), _i32(3, 2, 16, 16), torch.zeros((3, 2, 16, 4), dtype=torch.int16)
+
+    def paged_(x=k, slots=slots, codes=codes, norms=norms):
+        tq.quantize_kv_paged(rot, 4, kc, kt, x, slots, codes, norms, 16)
+    refused("not on a CUDA device", paged_)
+    refused("^slots:", paged_, slots=slots.int())
+    refused("^slots:", paged_, slots=slots[:3])
+    refused("^codes:", paged_, codes=_i32(3, 2, 16, 12))
+    refused("^codes:", paged_, codes=_i32(3, 1, 16, 16))
+    refused("^norms:", paged_, norms=norms.half())
+    refused("^norms:", paged_, norms=norms[:2])
+    refused("^x:", paged_, x=q[:, ::2])
+
+    pages = dict(k_codes=codes, k_norms=norms, v_codes=_i32(3, 2, 16, 12), v_norms=norms)
+    mask, ws = torch.zeros((4, 1), dtype=torch.int64), torch.zeros(256, dtype=torch.uint8)
+
+    def tree_(q=q, cu=_i32(3), lens=_i32(2), pages=pages, table=_i32(2, 4), mask=mask, **kw):
+        tq.tree_attention(rot, 4, 3, kc, vc, q, cu, lens, pages, table, 16, 2, 64, tree_mask=mask, workspace=ws, **kw)
+    refused("not on a CUDA device", tree_)
+    refused("^cu_nodes:", tree_, cu=_i32(2))
+    refused("^lens:", tree_, lens=_i32(2).long())
+    refused("^tree_mask:", tree_, mask=mask.int())
+    refused("^tree_mask:", tree_, mask=mask[:3])
+    refused("^tree_mask:", tree_, mask=mask[:, 0])
+    refused("^block_table:", tree_, table=_i32(3, 4))
+    refused("^q and out:", tree_, q=q[:, ::2])
+    refused("^q and out:", tree_, out=q.half())
+    for name in pages:
+        refused(f"^{name}:", tree_, pages=dict(pages, **{name: _i32(3, 2, 16, 5)}))
