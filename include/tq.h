@@ -551,13 +551,15 @@ tq_status tq_quantize_kv_paged(const tq_rotation * rot, int32_t bits, int32_t bl
  *               16-byte aligned; strides multiples of 8 and at least the row.
  *   dtype:      TQ_DTYPE_BF16 or TQ_DTYPE_F16, of q, k, v and out.
  *   cu_q, cu_k: device int32 [batch + 1], non-decreasing, from 0 to at most
- *               total_q / total_k (values outside are clamped into the arrays);
- *               cu_k NULL = cu_q.
- *   scale:      <= 0 selects 1/sqrt(head_dim).
+ *               total_q / total_k; cu_k NULL = cu_q.  Offsets outside are clamped
+ *               into the arrays and set TQ_STATUS_LIMIT; where a sequence ends
+ *               behind them, its queries that are there attend the same keys,
+ *               as far as those are there.
+ *   scale:      <= 0 selects 1/sqrt(head_dim).  total_q == 0 is a no-op.
  *   out:        device [total_q][n_q_heads][head_dim] of dtype, contiguous, 16-byte
  *               aligned; rows from cu_q[batch] on are left as they are.  Must not
  *               overlap q, k or v.
- *   status_dev: device uint32 or NULL (TQ_STATUS_TIMEOUT).
+ *   status_dev: device uint32 or NULL (TQ_STATUS_TIMEOUT, TQ_STATUS_LIMIT).
  * head_dim 64 / 128 / 256; n_q_heads a multiple of n_kv_heads; any group size;
  * total_q and total_k below 2^31 - 255.  Scores and sums are fp32; the
  * probabilities enter the second product rounded to dtype, the sum that divides

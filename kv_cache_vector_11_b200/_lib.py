@@ -531,7 +531,8 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, scale=0.0, out=None, status=None,
     be strided, as slices of a fused projection are), offsets cu_q and cu_k
     int32 [batch + 1] (cu_k defaults to cu_q).  With fewer queries than keys
     the queries are the last ones.  Returns out, of q's type and shape; rows
-    past cu_q[batch] are left as they are."""
+    past cu_q[batch] are left as they are.  Offsets past the arrays are cut there
+    and set STATUS_LIMIT in ``status``."""
     import torch
     total_q, n_q, d = q.shape
     total_k, n_kv, _ = k.shape

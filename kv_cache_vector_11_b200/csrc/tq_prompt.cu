@@ -204,7 +204,11 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         }
         return n;
     };
-    int seq = -1, tile = 0;
+    // Query i attends the keys below i + shift + 1, counted from where the sequence
+    // starts to where its offsets say that it ends, also behind the arrays: rows that
+    // are there then attend the same keys as they would if all were.
+    auto shift_of = [&](int b, int r0, int c0) { return (max(a.cu_k[b + 1], c0) - c0) - (max(a.cu_q[b + 1], r0) - r0); };
+    int seq = -1, tile = 0, shift = 0;
     int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
     if (a.batch <= 128) {
         // every warp for itself, without a barrier
@@ -225,6 +229,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                 q1 = __shfl_sync(0xffffffffu, r1, at);
                 k0 = __shfl_sync(0xffffffffu, c0, at);
                 k1 = __shfl_sync(0xffffffffu, c1, at);
+                shift = __shfl_sync(0xffffffffu, shift_of(b, r0, c0), at);
             }
             before = __shfl_sync(0xffffffffu, end, 31);
         }
@@ -258,13 +263,13 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             q1 = clamp_to(a.cu_q[seq + 1], q0, (int)a.total_q);
             k0 = clamp_to(a.cu_k[seq], 0, (int)a.total_k);
             k1 = clamp_to(a.cu_k[seq + 1], k0, (int)a.total_k);
+            shift = shift_of(seq, q0, k0);
         }
     }
     const int nq = q1 - q0, nk = k1 - k0;
     const int i0 = tile * cta_queries;                    // first query of this CTA
-    const int shift = nk - nq;                            // query i attends the keys below i + shift + 1
     const int i_last = min(i0 + cta_queries, nq) - 1;
-    const int n_keys = max(i_last + shift + 1, 0);        // (at most nk)
+    const int n_keys = min(max(i_last + shift + 1, 0), nk);
     // key tiles, taken from the last to the first; none past the last row tile
     const int n = seq < 0 ? 0 : (n_keys + kTile - 1) / kTile;
     const int full_keys = min(max(i0 + shift + 1, 0), nk);    // keys that every row attends
@@ -587,6 +592,12 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     __syncthreads();
     tc::fence_after_sync();
     if (*s_err != 0 && tid == 0 && a.status != nullptr) atomicOr(a.status, TQ_STATUS_TIMEOUT);
+    if (blockIdx.x == gridDim.x - 1 && a.status != nullptr) {        // (seldom has a tile)
+        for (int b = tid; b < a.batch; b += NT)
+            if (a.cu_q[b] < 0 || a.cu_q[b + 1] < a.cu_q[b] || a.cu_q[b + 1] > a.total_q || a.cu_k[b] < 0 ||
+                a.cu_k[b + 1] < a.cu_k[b] || a.cu_k[b + 1] > a.total_k)
+                atomicOr(a.status, TQ_STATUS_LIMIT);
+    }
     if (warp == 0) tc::tmem_dealloc(tmem, 512);
     if (*s_redo != 0) {
         __syncthreads();

@@ -292,3 +292,44 @@ def test_outputs_of_a_call_are_kept_for_the_current_stream(tq, which):
         later = [torch.full((n,), 0x3C, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(copies, want)) and len(later) == 3 * len(sizes)
+
+
+# -- prompt offsets past the arrays -----------------------------------------------------------
+
+@pytest.mark.parametrize("batch", [1, 40, 200])
+@pytest.mark.parametrize("d", [64, 256])
+def test_prompt_rows_past_the_arrays_leave_the_others(tq, batch, d):
+    """Offsets of a last sequence that end behind the arrays (a captured call replayed
+    with larger ones): its rows that are there attend what they attend in full arrays,
+    as far as it is there."""
+    rng = np.random.default_rng(batch + d)
+    cu = np.cumsum([0] + [3] * (batch - 1) + [150])
+    total, first = int(cu[-1]), int(cu[-2])
+    q, k, v = (torch.from_numpy(rng.standard_normal((total, h, d))).to("cuda", torch.bfloat16) for h in (4, 2, 2))
+    ref, absum, sq = osv.prompt_attention(f64(q), f64(k), f64(v), cu, cu)
+    for rows, keys in ((total, total), (total - 60, total), (total, total - 30), (total - 60, total - 30),
+                       (total - 150, total)):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = f64(tq.prompt_attention(q[:rows], k[:keys], v[:keys], i32(cu), i32(cu), status=status))
+        # (a call with no rows launches nothing)
+        assert int(status) == (0 if rows == 0 or rows == keys == total else tq.STATUS_LIMIT)
+        want, scale = ref[:rows].copy(), absum[:rows].copy()
+        for h in range(4):                                # the rows some of whose keys are missing
+            if rows > keys:
+                every = np.ones((rows - keys, keys - first), dtype=bool)
+                want[keys:, h], scale[keys:, h], _ = osv.attend(f64(q)[keys:rows, h], f64(k)[first:keys, h // 2],
+                                                                f64(v)[first:keys, h // 2], every, d**-0.5)
+        assert np.all(np.abs(got - want) <= S.prompt_bound(want, scale, sq[:rows], "bf16", d, 150))
+
+
+def test_prompt_offsets_past_the_arrays_are_reported(tq):
+    q = torch.randn((50, 2, 64), device="cuda").half()
+    for cu, cu_k in (([-1, 30, 50], None), ([0, 30, 51], None), ([0, 40, 10, 50], None), ([0, 30, 50], [-2, 30, 50]),
+                     ([0, 30, 50], [0, 31, 30]), ([0, 30, 50], [0, 30, 60]), ([0] * 300 + [51], None)):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        tq.prompt_attention(q, q, q, i32(cu), None if cu_k is None else i32(cu_k), status=status)
+        assert int(status) == tq.STATUS_LIMIT, (cu, cu_k)
+    for cu in ([0, 30, 50], [2, 2, 40], [0] * 300 + [50], [50, 50]):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        tq.prompt_attention(q, q, q, i32(cu), status=status)
+        assert int(status) == 0, cu
