@@ -162,6 +162,10 @@ class Rotation:
                "tq_make_rotation")
         self._h = h
         self.kind, self.rows, self.cols, self.seed = kind, rows, cols, seed
+        self.device = None                              # of the matrix; a WHT has none on the device
+        if kind != "wht":
+            import torch
+            self.device = torch.cuda.current_device()
 
     @property
     def handle(self):
@@ -400,6 +404,13 @@ def _ints(t, n, name, device, kind):
     return t.data_ptr()
 
 
+def _rotation(rot, device):
+    """Handle of a rotation whose matrix, if it has one, lies on ``device``."""
+    if rot.device is not None and rot.device != device.index:
+        raise ValueError(f"rotation: made on cuda:{rot.device}, used on {device}")
+    return rot.handle
+
+
 def _status_ptr(t, device):
     """Pointer of the status word (None: none is kept)."""
     import torch
@@ -519,7 +530,7 @@ def quantize_kv_paged(rot, bits, centroids, boundaries, x, slots, codes, norms, 
     slots_p = _ints(slots, n, "slots", dev, torch.int64)
     codes_p = _page_part(codes, "codes", torch.int32, (n_pages, heads, page_size, w), dev)
     norms_p = _page_part(norms, "norms", torch.int16, (n_pages, heads, page_size, d // 32), dev)
-    _launch(_lib.tq_quantize_kv_paged, "tq_quantize_kv_paged", dev, stream, rot.handle, bits, block,
+    _launch(_lib.tq_quantize_kv_paged, "tq_quantize_kv_paged", dev, stream, _rotation(rot, dev), bits, block,
             _host_floats(centroids, 1 << bits, "centroids"), _host_floats(boundaries, (1 << bits) - 1, "boundaries"),
             x.data_ptr(), _dtype_code(x), n, heads, d,
             slots_p, page_size, n_pages, codes_p, norms_p, _status_ptr(status, dev))
@@ -610,7 +621,7 @@ def tree_attention(rot, k_bits, v_bits, k_centroids, v_centroids, q, cu_nodes, l
             need = tree_workspace_size(batch, n_rows, max_nodes, n_q, n_kv, max_len, d)
         workspace = _empty((max(need, 256),), torch.uint8, dev, stream, returned=False)
     _require(workspace.device == dev and workspace.is_contiguous(), "workspace: contiguous, on q's device")
-    _launch(_lib.tq_tree_attention, "tq_tree_attention", dev, stream, rot.handle, k_bits, v_bits, block,
+    _launch(_lib.tq_tree_attention, "tq_tree_attention", dev, stream, _rotation(rot, dev), k_bits, v_bits, block,
             _host_floats(k_centroids, 1 << k_bits, "k_centroids"), _host_floats(v_centroids, 1 << v_bits, "v_centroids"),
             q.data_ptr(), _dtype_code16(q), cu_p, batch, n_rows, max_nodes, lens_p, max_len, mask_p, words, n_q, n_kv, d,
             page_size, n_pages, table_p, max_pages, *storage, float(scale), out.data_ptr(), workspace.data_ptr(),

@@ -292,3 +292,15 @@ def test_python_refusals_name_the_tensor(rot):
     refused("^q and out:", tree_, out=q.half())
     for name in pages:
         refused(f"^{name}:", tree_, pages=dict(pages, **{name: _i32(3, 2, 16, 5)}))
+
+
+def test_python_refuses_a_rotation_of_another_device(rot):
+    """A dense rotation's matrix lies on the device that it was made on."""
+    class Dense:
+        handle, device = rot.handle, 3
+    (kc, kt), vc = tq.build_codebook(4), tq.build_codebook(3)[0]
+    assert rot.device is None
+    with pytest.raises(ValueError, match="^rotation: made on cuda:3"):
+        _quantize_call(Dense, 4, kc, kt)
+    with pytest.raises(ValueError, match="^rotation: made on cuda:3"):
+        _tree_call(Dense, 4, 3, kc, vc)
