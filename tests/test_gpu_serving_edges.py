@@ -224,6 +224,27 @@ def test_tree_zero_queries_with_a_small_scale(tq, kernel):
     assert np.all(np.linalg.norm(f64(got) - ref, axis=-1) <= S.tree_bound(ref, absum, sq, "f32", d, max(t.lens)))
 
 
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("size", [1e-2, 1e-4, 1e-6])
+def test_tree_small_norms(tq, kernel, size):
+    """Dequantized values in fp16's subnormal range are rounded to a multiple of
+    2^-24: off by 2^-25 each, so by 2^-25 sqrt(d) a value row and by as much times
+    |q| and the scale a score, where S.tree_bound has 2^-11 of the value instead of
+    its absolute term for these.  Weights below 2^-21 of a row's largest are off by
+    2^-32 of it."""
+    n, hq, hk, d = KERNELS[kernel]
+    t = Tree(tq, [n, n], [n + 90, n + 300], hq, hk, d, dtype=torch.float32, norms=size)
+    got, status = t.call(n)
+    ref, absum, sq = t.reference()
+    row = 2.0**-25 * np.sqrt(d)
+    es = row * np.linalg.norm(f64(t.q), axis=-1) / np.sqrt(d)
+    longest = float(np.max(np.abs(t.cache["v_norms"].astype(np.float64)))) * np.sqrt(d / 32)
+    bound = S.tree_bound(ref, absum, sq, "f32", d, max(t.lens)) - 1e-6
+    bound = bound + row + np.expm1(2 * es) * absum + max(t.lens) * 2.0**-32 * longest
+    assert status == 0
+    assert np.all(np.linalg.norm(f64(got) - ref, axis=-1) <= bound)
+
+
 # -- calls on another stream ------------------------------------------------------------------
 
 def _busy(x, n=20):
