@@ -619,8 +619,7 @@ size_t tq_tree_workspace_size(int32_t batch, int32_t n_rows, int32_t max_nodes,
  * Block 32 with fp16 norms, default code order, keys without QJL signs.  The
  * rotated queries (scaled to one by row) and the dequantized rows enter the products
  * as fp16, so a dequantized value is off by 2^-11 of itself or, below 2^-14 (6.1e-5),
- * by 2^-25: a block whose norm is under some 1e-3 loses accuracy that
- * tq_decode_attention, which multiplies by norms in fp32, keeps.  Sums are fp32.  A
+ * by 2^-25: blocks with norms under some 1e-3 lose accuracy.  Sums are fp32.  A
  * cached token whose K or V norm is NaN or infinite makes the nodes that
  * attend it NaN, and no others; a query row that is not finite makes its own output
  * NaN.
