@@ -24,6 +24,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -110,10 +111,27 @@ def _code_only(text):
     return "".join("".join(out).split())
 
 
-def kernel_source_hash():
+def kernel_sources(kernel_key):
+    """The files of csrc that the kernels of a traffic entry are made of: their
+    .cu and the headers it includes (the other .cu files hold other kernels)."""
+    csrc = os.path.join(ROOT, "kv_cache_vector_11_b200", "csrc")
+    todo = ["tq_quantize.cu" if kernel_key.startswith("quantize_") else "tq_attention.cu"]
+    seen = []
+    while todo:
+        name = todo.pop()
+        if name in seen or not os.path.exists(os.path.join(csrc, name)):
+            continue
+        seen.append(name)
+        with open(os.path.join(csrc, name), encoding="utf-8") as f:
+            todo += re.findall(r'#include "(\w+\.\w+)"', f.read())
+    return sorted(seen)
+
+
+def kernel_source_hash(kernel_key=None):
+    """Hash of the sources of one traffic entry's kernels, or of all of csrc."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "kv_cache_vector_11_b200", "csrc")
-    for name in sorted(os.listdir(csrc)):
+    for name in sorted(os.listdir(csrc)) if kernel_key is None else kernel_sources(kernel_key):
         with open(os.path.join(csrc, name), encoding="utf-8") as f:
             h.update(name.encode())
             h.update(_code_only(f.read()).encode())
@@ -129,7 +147,7 @@ def ncu_traffic(kernel_key):
     with open(p) as f:
         d = json.load(f)
     ent = d.get(kernel_key)
-    if not ent or ent.get("source_hash") != kernel_source_hash():
+    if not ent or ent.get("source_hash") != kernel_source_hash(kernel_key):
         return None
     return ent.get("dram_bytes_per_launch")
 

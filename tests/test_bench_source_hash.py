@@ -2,6 +2,7 @@
 comment or whitespace edit leaves unchanged and a code edit changes."""
 
 import importlib.util
+import json
 import os
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -35,3 +36,18 @@ def test_hash_covers_the_kernel_sources():
     h = b.kernel_source_hash()
     assert isinstance(h, str) and len(h) == 16
     assert h == b.kernel_source_hash()
+
+
+def test_traffic_tags_cover_the_files_of_their_kernels():
+    b = _bench()
+    quant, decode = b.kernel_sources("quantize_rot_tc_kernel<128,4,false>"), b.kernel_sources("decode_mma_kernel")
+    assert quant == ["tq_device.cuh", "tq_internal.h", "tq_quantize.cu", "tq_tc.cuh"]
+    assert decode == ["tq_attention.cu", "tq_device.cuh", "tq_internal.h", "tq_tc.cuh"]
+    assert len({b.kernel_source_hash("quantize_"), b.kernel_source_hash("decode_"), b.kernel_source_hash()}) == 3
+
+
+def test_every_traffic_entry_is_of_the_current_sources():
+    b = _bench()
+    with open(os.path.join(ROOT, "profiles", "ncu_traffic.json"), encoding="utf-8") as f:
+        entries = [k for k in json.load(f) if not k.startswith("_")]
+    assert entries and all(b.ncu_traffic(k) for k in entries)
