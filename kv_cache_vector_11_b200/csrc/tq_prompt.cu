@@ -24,14 +24,16 @@
 // non-finite value inside it makes the CTA compute its rows again on the CUDA
 // cores, with the keys that a row attends and no others.
 //
-// What bounds it (8192 tokens, 32 / 8 heads, d = 128, bf16: 0.418 ms, 1.32 PFLOP/s,
-// 0.80 of the measured GEMM rate): the issue and wake-up latencies between the
-// softmax and the tensor core, which is busy three quarters of the time; leaving
-// the exponentials out gains 4 %, half the score products 10 %.  Taking turns
-// between the two issuing threads cost 7 %, score tiles of 128 keys at once
-// (instead of two halves) 13 %.  Short sequences are bound by a block's way in
-// and out, 4 us of loads, one softmax and the stores that nothing overlaps
-// (16 prompts of 64 .. 2048 tokens: 0.161 ms, of which 0.06 ms).
+// What bounds it (8192 tokens, 32 / 8 heads, d = 128, bf16: 0.418 ms on the same
+// inputs again and again, 1.32 PFLOP/s, 0.80 of the measured burst rate of a GEMM;
+// 0.494 ms on inputs that change, 1.11 PFLOP/s, 0.79 of its sustained rate): the
+// issue and wake-up latencies between the softmax and the tensor core, whose pipe is
+// active 66 % of the cycles; leaving the exponentials out gains 4 %, half the score
+// products 10 %.  Taking turns between the two issuing threads cost 7 %, score tiles
+// of 128 keys at once (instead of two halves) 13 %.  Short sequences are bound by a
+// block's way in and out, 4 us of loads, one softmax and the stores that nothing
+// overlaps (16 prompts of 64 .. 2048 tokens: 0.161 ms on the same inputs, of which
+// 0.06 ms; 0.176 ms on inputs that change).
 
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -37,7 +37,8 @@
 // What bounds it: the integer pipe, which byte permutes, masks and the maxima of
 // the softmax share.  A key tile of 128 tokens takes the two unpacking warpgroups
 // about 3000 cycles (d = 128, 4-bit keys and 3-bit values), its products 1280 a
-// row tile; 8 x 128K trees of 64 nodes, 4 heads a group: 1.21 ms, 0.91 PFLOP/s.
+// row tile; 8 x 128K trees of 64 nodes, 4 heads a group: 1.21 ms on the same inputs
+// again and again, 0.91 PFLOP/s; 1.39 ms on inputs that change, 0.79 PFLOP/s.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
