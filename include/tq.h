@@ -611,7 +611,8 @@ size_t tq_tree_workspace_size(int32_t batch, int32_t n_rows, int32_t max_nodes,
  *   block_table, page_size, n_pages, k_*, v_*: as in tq_decode_append_paged
  *               (entries outside [0, n_pages) are clamped), fewer than 2^32 rows
  *               (n_pages * n_kv_heads * page_size).
- *   out:        device [n_rows][n_q_heads][head_dim] of q_dtype, 16-byte aligned.
+ *   out:        device [n_rows][n_q_heads][head_dim] of q_dtype, 16-byte aligned; may
+ *               be q.
  *   workspace:  >= tq_tree_workspace_size(...) bytes for these sizes, 256-byte
  *               aligned, needs no initialisation; calls that may overlap need one
  *               each.

@@ -354,3 +354,161 @@ def test_prompt_offsets_past_the_arrays_are_reported(tq):
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
         tq.prompt_attention(q, q, q, i32(cu), status=status)
         assert int(status) == 0, cu
+
+
+# -- more of what the calls allow -------------------------------------------------------------
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_tree_in_place(tq, kernel):
+    """out may be q: the queries are read before the first output is written."""
+    n, hq, hk, d = KERNELS[kernel]
+    t = Tree(tq, [n, n], [n + 90, n + 700], hq, hk, d)
+    want, _ = t.call(n)
+    q = t.q.clone()
+    got, status = t.call(n, q=q, out=q)
+    assert status == 0 and got is q and torch.equal(got, want)
+
+
+def test_tree_wide_groups_and_many_requests(tq):
+    t = Tree(tq, [40, 3], [300, 170], 64, 1, 64)
+    got, status = t.call(40)
+    ref, absum, sq = t.reference()
+    assert status == 0 and np.all(np.linalg.norm(f64(got) - ref, axis=-1) <= S.tree_bound(ref, absum, sq, "bf16", 64, 300))
+    rng = np.random.default_rng(5)
+    lens = rng.integers(0, 60, 3000).tolist()
+    t = Tree(tq, [min(1, x) for x in lens], lens, 2, 2, 64)
+    got, status = t.call(1)
+    ref, absum, sq = t.reference()
+    assert status == 0 and np.all(np.linalg.norm(f64(got) - ref, axis=-1) <= S.tree_bound(ref, absum, sq, "bf16", 64, 60))
+
+
+@pytest.mark.parametrize("group", [33, 37, 48, 64])
+def test_prompt_wide_groups(tq, group):
+    """Groups whose heads do not fit one row tile, a prime one among them."""
+    rng = np.random.default_rng(group)
+    q, k, v = (torch.from_numpy(rng.standard_normal((70, h, 64))).to("cuda", torch.bfloat16) for h in (group, 1, 1))
+    cu = [0, 1, 70]
+    got = f64(tq.prompt_attention(q, k, v, i32(cu)))
+    ref, absum, sq = osv.prompt_attention(f64(q), f64(k), f64(v), cu, cu)
+    assert np.all(np.abs(got - ref) <= S.prompt_bound(ref, absum, sq, "bf16", 64, 69))
+
+
+def test_page_tables_largest_batch(tq):
+    rng = np.random.default_rng(6)
+    batch, page = 16384, 16
+    ctx, new = rng.integers(0, 50, batch), rng.integers(0, 9, batch)
+    held, want = -(-ctx // page), -(-(ctx + new) // page)
+    n_pages = int(want.sum())
+    perm = rng.permutation(n_pages)
+    table = np.full((batch, 4), -1, dtype=np.int32)
+    table[np.arange(4)[None, :] < held[:, None]] = perm[:held.sum()]
+    free, n_slots = perm[held.sum():], int(new.sum()) + 3
+    t = i32(table)
+    out = tq.page_tables(i32(ctx), i32(new), page, n_pages, i32(free), t, n_slots)
+    ref = osv.page_tables(ctx, new, page, n_pages, free, table, n_slots)
+    for name, x in dict(out, block_table=t).items():
+        assert np.array_equal(x.cpu().numpy(), ref[name]), name
+
+
+def test_calls_without_tokens(tq):
+    t = Tree(tq, [0, 0], [30, 0], 4, 2, 64)
+    assert t.call(1)[1] == 0                                   # no rows
+    q = torch.zeros((5, 4, 64), device="cuda").bfloat16()
+    out, status = t.call(1, q=q)                               # rows of padding only
+    assert status == 0 and bool((out == 7.0).all())
+    none = torch.empty((0, 4, 64), device="cuda").bfloat16()
+    assert tq.prompt_attention(none, none, none, i32([0, 0])).shape == none.shape
+    got = tq.prompt_attention(q, none, none, i32([0, 5]), i32([0, 0]))
+    assert bool((got == 0).all())                              # queries without a key
+    kc, kt = tq.build_codebook(4)
+    before = {k: v.clone() for k, v in t.pages.items()}
+    tq.quantize_kv_paged(t.rot, 4, kc, kt, none[:, :2].contiguous(), torch.empty(0, dtype=torch.int64, device="cuda"),
+                         t.pages["k_codes"], t.pages["k_norms"], t.page)
+    assert all(torch.equal(before[k], v) for k, v in t.pages.items())
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_offsets_past_32_bits_in_the_cache(tq, kernel):
+    """Rows whose codes lie more than 2^32 bytes into the page storage are stored
+    and read as in a small one."""
+    n, hq, hk, d = KERNELS[kernel]
+    page, bits, lens = 256, 4, [600, 300]
+    per = [-(-x // page) for x in lens]
+    small, wide = sum(per), (2**32 + 2**28) // (hk * page * d * bits // 8)
+    rng = np.random.default_rng(d)
+    rot = tq.Rotation("wht", d, d, W.SEED_ROT)
+    kc, kt = tq.build_codebook(bits)
+    rows = torch.from_numpy(rng.standard_normal((2, sum(lens), hk, d))).to("cuda", torch.bfloat16)
+    q = torch.from_numpy(rng.standard_normal((2 * n, hq, d))).to("cuda", torch.bfloat16)
+    out = []
+    for n_pages in (small, wide):
+        pages = {}
+        for name in "kv":
+            pages[name + "_codes"] = torch.zeros((n_pages, hk, page, d * bits // 32), dtype=torch.int32, device="cuda")
+            pages[name + "_norms"] = torch.zeros((n_pages, hk, page, d // 32), dtype=torch.int16, device="cuda")
+        ids = np.arange(n_pages - small, n_pages)
+        table = np.zeros((2, max(per)), dtype=np.int64)
+        table[0, :per[0]], table[1, :per[1]] = ids[:per[0]], ids[per[0]:]
+        t = [np.arange(x) for x in lens]
+        slots = np.concatenate([table[b][t[b] // page] * page + t[b] % page for b in range(2)])
+        for i, name in enumerate("kv"):
+            tq.quantize_kv_paged(rot, bits, kc, kt, rows[i], torch.from_numpy(slots).cuda(), pages[name + "_codes"],
+                                 pages[name + "_norms"], page)
+        out.append(tq.tree_attention(rot, bits, bits, kc, kc, q, i32([0, n, 2 * n]), i32(lens), pages, i32(table), page, n,
+                                     max(lens)))
+        del pages
+    assert torch.equal(out[0], out[1]) and float(out[0].abs().max()) > 0
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_prompt_offsets_past_32_bits(tq, d):
+    """Rows that lie more than 2^32 elements into a fused projection."""
+    heads, total, n = (16, 8, 8), 2**32 // (32 * d) + 700, 300
+    qkv = torch.zeros((total, sum(heads), d), dtype=torch.bfloat16, device="cuda")
+    qkv[-n:] = torch.randn((n, sum(heads), d), device="cuda").bfloat16()
+    out = torch.zeros((total, heads[0], d), dtype=torch.bfloat16, device="cuda")
+    q, k, v = qkv[:, :16], qkv[:, 16:24], qkv[:, 24:]
+    tq.prompt_attention(q, k, v, i32([total - n, total - 100, total]), out=out)
+    want = tq.prompt_attention(q[-n:], k[-n:], v[-n:], i32([0, n - 100, n]))
+    assert torch.equal(out[-n:], want) and not bool(out[:-n].any())
+
+
+def test_a_captured_step_replayed_with_other_lengths(tq):
+    """Tables, stores and drafted-token attention of a step in one graph, rows padded to
+    its size: every replay gives what the calls give for its lengths."""
+    rng = np.random.default_rng(8)
+    d, hq, hk, page, n_pages, rows = 128, 8, 2, 16, 64, 12
+    rot = tq.Rotation("wht", d, d, W.SEED_ROT)
+    (kc, kt), (vc, vt) = tq.build_codebook(4), tq.build_codebook(3)
+    start = S.cache_to(S.random_cache(rng, n_pages, hk, page, d, 4, 3), "cuda")
+    perm = rng.permutation(n_pages)
+    first = np.full((2, 16), -1, dtype=np.int32)
+    first[0, :10], first[1, :10] = perm[:10], perm[10:20]
+    free = i32(perm[20:])
+    ctx, new, table = i32([0, 0]), i32([0, 0]), i32(first)
+    pages = {k: v.clone() for k, v in start.items()}
+    q, k, v = (torch.from_numpy(rng.standard_normal((rows, h, d))).to("cuda", torch.bfloat16) for h in (hq, hk, hk))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def step(table, pages, out):
+        t = tq.page_tables(ctx, new, page, n_pages, free, table, rows, status=status)
+        tq.quantize_kv_paged(rot, 4, kc, kt, k, t["slots"], pages["k_codes"], pages["k_norms"], page, status=status)
+        tq.quantize_kv_paged(rot, 3, vc, vt, v, t["slots"], pages["v_codes"], pages["v_norms"], page, status=status)
+        return tq.tree_attention(rot, 4, 3, kc, vc, q, t["cu_new"], t["total_lens"], pages, table, page, 8, 256, out=out,
+                                 status=status)
+    out = torch.zeros_like(q)
+    step(table, pages, out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(table, pages, out)
+    for c, n in (([150, 33], [8, 4]), ([16, 160], [1, 1]), ([0, 159], [3, 0]), ([47, 48], [2, 7])):
+        ctx.copy_(i32(c)), new.copy_(i32(n)), table.copy_(i32(first)), out.fill_(7.0)
+        for name in pages:
+            pages[name].copy_(start[name])
+        g.replay()
+        fresh = {name: x.clone() for name, x in start.items()}
+        want = step(i32(first), fresh, torch.full_like(q, 7.0))
+        torch.cuda.synchronize()
+        assert int(status) == 0 and torch.equal(out, want), (c, n)
+        assert all(torch.equal(pages[name], fresh[name]) for name in pages)
+        assert bool((out[sum(n):] == 7.0).all()) and bool((out[:sum(n)] != 7.0).any())
