@@ -133,6 +133,22 @@ def _on(device):
     return torch.cuda.device(device)
 
 
+def _empty(shape, dtype, device, stream, returned=True):
+    """Memory that a call on ``stream`` allocates itself.  It comes from that
+    stream's own blocks: one that the current stream gave back may still be read
+    or written there, by work which ``stream`` does not wait for.  What the call
+    returns is used on the current stream, and not given out again before that
+    stream is done with it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def rotation_generate(kind, rows, cols, seed):
     """Dense float64 matrix of a seeded rotation / projection (host only)."""
     out = np.empty((rows, cols), dtype=np.float64)
@@ -223,12 +239,11 @@ def quantize_kv(rot, bits, centroids, boundaries, x, qjl=None, block=32, out=Non
     w = max(code_words_per_row(bits, block, d), 0)   # -1 for an unsupported block: the call rejects it
     dev = x.device
     if out is None:
-        out = {"codes": torch.empty((n, w), dtype=torch.int32, device=dev),
-               "norms": torch.empty((n, max(d // block, 0)),
-                                    dtype=torch.float32 if norm_f32 else torch.int16, device=dev)}
+        out = {"codes": _empty((n, w), torch.int32, dev, stream),
+               "norms": _empty((n, max(d // block, 0)), torch.float32 if norm_f32 else torch.int16, dev, stream)}
         if qjl is not None:
-            out["signs"] = torch.empty((n, qjl.rows // 32), dtype=torch.int32, device=dev)
-            out["rnorm"] = torch.empty((n,), dtype=torch.int16, device=dev)
+            out["signs"] = _empty((n, qjl.rows // 32), torch.int32, dev, stream)
+            out["rnorm"] = _empty((n,), torch.int16, dev, stream)
     c = np.ascontiguousarray(centroids, dtype=np.float32)
     t = np.ascontiguousarray(boundaries, dtype=np.float32)
     with _on(dev):
@@ -248,7 +263,7 @@ def attn_logits(rot, k_bits, k_centroids, q, k_codes, k_norms, n_kv_heads, ctx, 
     import torch
     batch, n_q, d = q.shape
     if logits is None:
-        logits = torch.empty((batch, n_q, ctx), dtype=torch.float32, device=q.device)
+        logits = _empty((batch, n_q, ctx), torch.float32, q.device, stream)
     c = np.ascontiguousarray(k_centroids, dtype=np.float32)
     with _on(q.device):
         _check(_lib.tq_attn_logits_ex(
@@ -272,11 +287,11 @@ def decode_attention(rot, k_bits, v_bits, k_centroids, v_centroids, q, k_codes, 
     import torch
     batch, n_q, d = q.shape
     if out is None:
-        out = torch.empty((batch, n_q, d), dtype=torch.float32, device=q.device)
+        out = _empty((batch, n_q, d), torch.float32, q.device, stream)
     with _on(q.device):
         need = decode_workspace_size(batch, n_q, n_kv_heads, ctx, d)
         if workspace is None:
-            workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=q.device)
+            workspace = _empty((max(need, 16),), torch.uint8, q.device, stream, returned=False)
         kc = np.ascontiguousarray(k_centroids, dtype=np.float32)
         vc = np.ascontiguousarray(v_centroids, dtype=np.float32)
         _check(_lib.tq_decode_attention_ex(
@@ -308,7 +323,7 @@ def decode_attention_static(rot, k_bits, v_bits, k_centroids, v_centroids, q, k_
     import torch
     batch, n_q, d = q.shape
     if out is None:
-        out = torch.empty((batch, n_q, d), dtype=torch.float32, device=q.device)
+        out = _empty((batch, n_q, d), torch.float32, q.device, stream)
     kc = np.ascontiguousarray(k_centroids, dtype=np.float32)
     vc = np.ascontiguousarray(v_centroids, dtype=np.float32)
     with _on(q.device):
@@ -334,13 +349,13 @@ def search_topk(rot, bits, centroids, q, db_codes, db_norms, k, block=32, worksp
     import torch
     n_q, d = q.shape
     n_db = db_codes.shape[0]
-    scores = torch.empty((n_q, k), dtype=torch.float32, device=q.device)
-    rows = torch.empty((n_q, k), dtype=torch.int32, device=q.device)
+    scores = _empty((n_q, k), torch.float32, q.device, stream)
+    rows = _empty((n_q, k), torch.int32, q.device, stream)
     c = np.ascontiguousarray(centroids, dtype=np.float32)
     with _on(q.device):
         need = search_workspace_size(n_q, n_db, d, k)
         if workspace is None:
-            workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=q.device)
+            workspace = _empty((max(need, 256),), torch.uint8, q.device, stream, returned=False)
         _check(_lib.tq_search_topk(
             rot.handle, bits, block, c.ctypes.data, _ptr(q), _dtype_code(q), n_q, d,
             _ptr(db_codes), _ptr(db_norms), n_db, k, _ptr(scores), _ptr(rows), _ptr(workspace),
@@ -362,7 +377,7 @@ def decode_append_paged(rot, k_bits, v_bits, k_codebook, v_codebook, q, k_new, v
     import torch
     batch, n_q, d = q.shape
     if out is None:
-        out = torch.empty((batch, n_q, d), dtype=torch.float32, device=q.device)
+        out = _empty((batch, n_q, d), torch.float32, q.device, stream)
     kc = np.ascontiguousarray(k_codebook[0], dtype=np.float32)
     kt = np.ascontiguousarray(k_codebook[1], dtype=np.float32)
     vc = np.ascontiguousarray(v_codebook[0], dtype=np.float32)
@@ -371,7 +386,7 @@ def decode_append_paged(rot, k_bits, v_bits, k_codebook, v_codebook, q, k_new, v
     with _on(q.device):
         need = decode_workspace_size(batch, n_q, n_kv_heads, ctx, d)
         if workspace is None:
-            workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=q.device)
+            workspace = _empty((max(need, 16),), torch.uint8, q.device, stream, returned=False)
         _check(_lib.tq_decode_append_paged(
             rot.handle, k_bits, v_bits, 32, kc.ctypes.data, kt.ctypes.data, vc.ctypes.data,
             vt.ctypes.data, _ptr(q), _dtype_code(q), _ptr(k_new), _ptr(v_new), _dtype_code(k_new),
@@ -444,22 +459,6 @@ def _stream_of(device):
     import torch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
-
-
-def _empty(shape, dtype, device, stream, returned=True):
-    """Memory that a call on ``stream`` allocates itself.  It comes from that
-    stream's own blocks: one that the current stream gave back may still be read
-    or written there, by work which ``stream`` does not wait for.  What the call
-    returns is used on the current stream, and not given out again before that
-    stream is done with it."""
-    import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if returned:
-        t.record_stream(torch.cuda.current_stream(device))
-    return t
 
 
 def _launch(fn, where, device, stream, *args):
