@@ -554,7 +554,8 @@ struct TaCfg {
     static constexpr int R_SOFTMAX = WGS == 2 ? 136 : 168;
     static constexpr int R_UNPACK = WGS == 2 ? 80 : 120;
     static constexpr int R_MMA = WGS == 2 ? 48 : 104;
-    static_assert(WGS * R_SOFTMAX + 2 * R_UNPACK + R_MMA <= (WGS == 2 ? 480 : 512), "no more than the launch holds");
+    static constexpr int R_LAUNCH = WGS == 2 ? 96 : 128;
+    static_assert(WGS * R_SOFTMAX + 2 * R_UNPACK + R_MMA <= (WGS + 3) * R_LAUNCH, "no more than the launch holds");
 };
 
 template <int N>
@@ -1566,6 +1567,13 @@ int launch_tree_main(const TreeArgs & a, cudaStream_t st) {
                               CU_TENSOR_MAP_SWIZZLE_128B))
         return (int)cudaErrorInvalidValue;
     auto k = tree_kernel<D, MODE>;
+    // a build that gives the kernel fewer registers would wait for good where the
+    // softmax warps take theirs
+    static const int regs = [] {
+        cudaFuncAttributes fa{};
+        return cudaFuncGetAttributes(&fa, tree_kernel<D, MODE>) == cudaSuccess ? fa.numRegs : 0;
+    }();
+    if (regs < C::R_LAUNCH) return (int)cudaErrorInvalidConfiguration;
     if (int e = ensure_dynamic_smem(reinterpret_cast<const void *>(k), C::SMEM)) return e;
     return launch_dependent(k, (unsigned)a.n_ctas, C::THREADS, C::SMEM, st, a, qmap);
 }
